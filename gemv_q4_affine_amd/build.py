@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libq4.so")
 
 SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "gemm_big.hip", "gemm_q8.hip", "affine8.hip", "noalloc.hip",
-           "capi.cpp"]
+           "capi.cpp", "block_simple.hip", "block_capi.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -127,7 +127,7 @@ def _compile_san(src: str) -> str:
 
 def build_host_sanitized(verbose: bool = False) -> str:
     """Build SAN_LIB if any source is newer than it; return its path."""
-    srcs = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "q4.h")]
+    srcs = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in ("q4.h", "q4_block.h")]
     if os.path.exists(SAN_LIB) and os.path.getmtime(SAN_LIB) >= max(os.path.getmtime(f) for f in srcs):
         return SAN_LIB
     os.makedirs(SAN_DIR, exist_ok=True)
