@@ -1,115 +1,7 @@
-// block_simple.hip -- the feed-forward operators in their simplest form: one
-// output per thread in binary32, weights dequantised element by element.
+// block_simple.hip -- block_norm and its gradients in their simplest form.
 #include "block_common.hpp"
 
 namespace q4 {
-
-__device__ __forceinline__ float weight(int wf, const QuantW& w, int64_t n, int64_t k, int64_t K) {
-    if (wf == WF_Q4_0) {
-        const int64_t b = n * (K / 32) + k / 32;
-        const int i = (int)(k & 31);
-        const int q = (w.q[b * 16 + (i & 15)] >> (i >= 16 ? 4 : 0)) & 15;
-        return (float)(q - 8) * f16_to_f32(w.s[b]);
-    }
-    const int64_t g = n * (K / 64) + k / 64;
-    const int q = wf == WF_AFFINE8 ? w.q[n * K + k] : (w.q[(n * K + k) / 2] >> (k & 1 ? 4 : 0)) & 15;
-    return fmaf((float)q, bf16_to_f32(w.s[g]), bf16_to_f32(w.b[g]));
-}
-
-__global__ void k_linear_simple(const LinearArgs a) {
-    __shared__ float xs[16][17], ws[2][16][17];
-    const int tx = threadIdx.x, ty = threadIdx.y;
-    const int64_t n = (int64_t)blockIdx.x * 16 + tx, m = (int64_t)blockIdx.y * 16 + ty;
-    const int64_t nw = (int64_t)blockIdx.x * 16 + ty;          // the weight row this thread stages
-    float acc[2] = {0.0f, 0.0f};
-    for (int64_t k0 = 0; k0 < a.K; k0 += 16) {
-        xs[ty][tx] = m < a.M ? load_elem(a.x, a.dtype, m * a.K + k0 + tx) : 0.0f;
-        for (int i = 0; i < a.nmat; i++) ws[i][ty][tx] = nw < a.N ? weight(a.wf, a.w[i], nw, k0 + tx, a.K) : 0.0f;
-        __syncthreads();
-        for (int i = 0; i < a.nmat; i++)
-            for (int k = 0; k < 16; k++) acc[i] = fmaf(xs[ty][k], ws[i][tx][k], acc[i]);
-        __syncthreads();
-    }
-    if (m >= a.M || n >= a.N) return;
-    const int64_t o = m * a.N + n;
-    for (int i = 0; i < a.nmat; i++) {
-        if (a.bias[i]) acc[i] += load_elem(a.bias[i], a.dtype, n);
-        if (a.pre[i]) store_elem(a.pre[i], a.dtype, o, acc[i]);
-    }
-    float v = activate(a.act, acc[0]);
-    if (a.nmat == 2) v *= acc[1];
-    if (a.residual) v += load_elem(a.residual, a.dtype, o);
-    store_elem(a.y, a.dtype, o, v);
-}
-
-// The gradient of projection i at (m, n).
-__device__ __forceinline__ float grad_elem(const LinearGradArgs& a, int i, int64_t o) {
-    const float dy = load_elem(a.dy, DT_BF16, o);
-    if (a.act == ACT_NONE && a.nmat == 1) return dy;
-    float slope;
-    const float v = activate<true>(a.act, load_elem(a.pre[0], DT_BF16, o), slope);
-    if (a.nmat == 1) return dy * slope;
-    return i == 0 ? dy * load_elem(a.pre[1], DT_BF16, o) * slope : dy * v;
-}
-
-__global__ void k_linear_dx_simple(const LinearGradArgs a) {
-    __shared__ float zs[16][17], ws[16][17];
-    const int tx = threadIdx.x, ty = threadIdx.y;
-    const int64_t k = (int64_t)blockIdx.x * 16 + tx, m = (int64_t)blockIdx.y * 16 + ty;
-    float acc = 0.0f;
-    for (int i = 0; i < a.nmat; i++)
-        for (int64_t n0 = 0; n0 < a.N; n0 += 16) {
-            zs[ty][tx] = m < a.M && n0 + tx < a.N ? grad_elem(a, i, m * a.N + n0 + tx) : 0.0f;
-            ws[ty][tx] = n0 + ty < a.N ? weight(a.wf, a.w[i], n0 + ty, k, a.K) : 0.0f;   // K % 16 == 0
-            __syncthreads();
-            for (int t = 0; t < 16; t++) acc = fmaf(zs[ty][t], ws[t][tx], acc);
-            __syncthreads();
-        }
-    if (m < a.M) store_elem(a.dx, DT_BF16, m * a.K + k, acc);
-}
-
-// dz, and its column sums: one thread per column and projection.
-__global__ void k_linear_dz_simple(const LinearGradArgs a) {
-    const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int i = blockIdx.y;
-    if (n >= a.N) return;
-    float sum = 0.0f;
-    for (int64_t m = 0; m < a.M; m++) {
-        const float v = grad_elem(a, i, m * a.N + n);
-        if (a.dz[i]) store_elem(a.dz[i], DT_BF16, m * a.N + n, v);
-        sum += v;
-    }
-    if (a.dbias[i]) a.dbias[i][n] = sum;
-}
-
-int64_t linear_workspace_bytes(int, int, int64_t, int64_t, int64_t) { return 0; }
-int64_t linear_grad_workspace_bytes(int, int, int64_t, int64_t, int64_t) { return 0; }
-
-hipError_t launch_linear(const LinearArgs& a, void*, hipStream_t s) {
-    for (int64_t m0 = 0; m0 < a.M; m0 += 16 * 65535) {
-        LinearArgs t = a;
-        t.M = a.M - m0 < 16 * 65535 ? a.M - m0 : 16 * 65535;
-        auto at = [&](const void* p, int64_t w) {
-            return p ? const_cast<void*>(static_cast<const void*>(static_cast<const char*>(p) + m0 * w * 2)) : nullptr;
-        };
-        t.x = at(a.x, a.K);
-        t.y = at(a.y, a.N);
-        t.residual = at(a.residual, a.N);
-        t.pre[0] = at(a.pre[0], a.N);
-        t.pre[1] = at(a.pre[1], a.N);
-        hipLaunchKernelGGL(k_linear_simple, dim3((unsigned)((a.N + 15) / 16), (unsigned)((t.M + 15) / 16)), dim3(16, 16),
-                           0, s, t);
-    }
-    return hipGetLastError();
-}
-
-hipError_t launch_linear_grad(const LinearGradArgs& a, void*, hipStream_t s) {
-    if (a.M > 16 * 65535) return hipErrorInvalidValue;
-    if (a.N > 0)
-        hipLaunchKernelGGL(k_linear_dz_simple, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(64), 0, s, a);
-    hipLaunchKernelGGL(k_linear_dx_simple, dim3((unsigned)(a.K / 16), (unsigned)((a.M + 15) / 16)), dim3(16, 16), 0, s, a);
-    return hipGetLastError();
-}
 
 // ---- norms: one workgroup per row --------------------------------------------
 

@@ -1,0 +1,310 @@
+// tile_gemm.hip -- the dense matrix-core product behind q4_linear, q4_gated
+// and their gradients at many rows: Z[m][n] = sum_k X[m][k] W[n][k] over two
+// binary16 images (tile_image.hpp), binary32 accumulation, with the operator's
+// epilogue on the accumulators.
+//
+// A workgroup of four waves owns a tile of 2 NT x 2 MT panels (NT = MT = 4: 256
+// columns x 256 rows); each wave owns NT x MT panels, that is NT MT accumulator
+// tiles of 32 x 32 in the AGPRs: at 4 x 4 all 256 of them, one wave per SIMD.
+// Per slice of 16 a wave reads NT + MT fragments for NT MT MFMAs, so at 4 x 4
+// the CU reads 64 KiB and copies 32 KiB per 1024 MFMA cycles, 94 bytes a cycle
+// of the about 110 that LDS moves; 8 waves of 4 x 2 would read 96 KiB.
+//
+// The sum runs in steps of two slices through a ring of four LDS slots that
+// direct-to-LDS copies fill up to four steps ahead.  In a step:
+//   slice 0: its MFMAs, and between the first ones the reads of slice 1;
+//   wait for the copies of the next step (two later ones stay in flight), and
+//   meet at the barrier: every wave has read this step, its slot is free;
+//   slice 1: its MFMAs, the reads of the next step's slice 0, and between the
+//   last ones the copies of the step after next but two, into the free slot.
+// One barrier per 1024 MFMA cycles; no read waits on a copy it does not need.
+// The order is written out and fenced: left alone, the compiler groups the
+// reads and copies and the matrix pipe runs dry behind them.
+//
+// The epilogue passes the accumulators through LDS, 32 rows at a time, so that
+// bias, residual and outputs move as whole rows of 16 bytes a lane.
+#include "tile_image.hpp"
+
+namespace q4 {
+
+constexpr int kRing = 4;
+
+// One direct-to-LDS copy of a unit: lane l's 16 bytes at src + 16 l land at LDS
+// address m0 + 16 l.  Inline assembly, so that the compiler does not take it
+// for an LDS store and wait for every copy in flight before each read; the
+// ring's own waits order the copies with the reads.  No register receives data.
+__device__ __forceinline__ void copy_unit(const uint8_t* src, uint32_t voff, uint32_t m0) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(src), "s"(m0)
+                 : "memory", "m0");
+}
+
+template <int NT, int MT, int EPI>
+__global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
+    static_assert(EPI != EPI_GATED || NT % 2 == 0, "gate and up panels come in pairs");
+    constexpr int kPanels = 2 * (NT + MT);                  // of a slot: weights first
+    constexpr int kSlot = kPanels * 2 * kUnit;              // [panel][slice][unit]
+    constexpr int kCopies = NT + MT;                        // of a wave and step
+    constexpr int kRowF = NT * 32 + 4;                      // a row of the epilogue's LDS tile, floats
+    constexpr int kLds = kRing * kSlot > 4 * 32 * kRowF * 4 ? kRing * kSlot : 4 * 32 * kRowF * 4;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave & 1, wm = wave >> 1;
+
+    // ---- the tile ------------------------------------------------------------
+    // Workgroup b runs on XCD b mod 8: consecutive tiles v go to one XCD, and
+    // run down the rows first, in groups of eight row tiles, so that an XCD's
+    // workgroups share a few row and column panels in its L2.
+    const int64_t tiles_n = (a.w_panels + 2 * NT - 1) / (2 * NT), tiles_m = (a.x_panels + 2 * MT - 1) / (2 * MT);
+    const int64_t G = gridDim.x, xcd = blockIdx.x % 8, each = G / 8, rest = G % 8;
+    int64_t v = xcd * each + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+    const int part = (int)(v / (tiles_n * tiles_m));
+    v -= part * (tiles_n * tiles_m);
+    const int64_t group = v / (8 * tiles_n), left_m = tiles_m - group * 8;
+    const int64_t high = left_m < 8 ? left_m : 8;
+    v -= group * 8 * tiles_n;
+    const int64_t pn0 = v / high * (2 * NT), pm0 = (group * 8 + v % high) * (2 * MT);
+
+    // ---- copies: unit t of this wave is slice (wave & 1) of panel (wave >> 1) + 2 t ----
+    const int64_t steps_all = a.slices / 2;
+    const int64_t s0 = steps_all * part / a.parts;
+    const int64_t S = steps_all * (part + 1) / a.parts - s0;
+    const uint8_t* src[kCopies];
+#pragma unroll
+    for (int t = 0; t < kCopies; t++) {
+        const int p = (wave >> 1) + 2 * t;
+        const bool w = p < 2 * NT;
+        // a panel past the image repeats its last one: those columns or rows are never stored
+        const int64_t last = (w ? a.w_panels : a.x_panels) - 1, pp = w ? pn0 + p : pm0 + p - 2 * NT;
+        src[t] = (w ? a.wimg : a.ximg) + ((pp < last ? pp : last) * a.slices + 2 * s0 + (wave & 1)) * kUnit;
+    }
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds) +
+                          (uint32_t)((wave >> 1) * 2 + (wave & 1)) * kUnit;
+    const uint32_t voff = (uint32_t)lane * 16;
+    // copy t of the next step to request, into slot; after the last step the
+    // last one is copied again (and never read), so that a wait counts alike
+    int64_t ahead = 0;                                       // step the pointers stand at
+    auto copy = [&](int t, int slot) __attribute__((always_inline)) {
+        copy_unit(src[t], voff, lds0 + (uint32_t)slot * kSlot + (uint32_t)t * 4 * kUnit);
+    };
+    auto advance = [&]() __attribute__((always_inline)) {
+        ahead++;
+        const int64_t by = ahead < S ? 2 * kUnit : 0;
+#pragma unroll
+        for (int t = 0; t < kCopies; t++) src[t] += by;
+    };
+
+    floatx16_t acc[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int j = 0; j < MT; j++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+
+    // fragments of a slice: weights 0 .. NT-1, then x
+    u32x4_t fa[NT + MT], fb[NT + MT];
+    auto read = [&](int f, int slot, int slice, u32x4_t (&fr)[NT + MT]) __attribute__((always_inline)) {
+        const int panel = f < NT ? wn * NT + f : 2 * NT + wm * MT + (f - NT);
+        fr[f] = *reinterpret_cast<const u32x4_t*>(lds + slot * kSlot + (panel * 2 + slice) * kUnit + lane * 16);
+    };
+    auto mfma = [&](int q, const u32x4_t (&fr)[NT + MT]) __attribute__((always_inline)) {
+        const int i = q / MT, j = q % MT;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, fr[i]),
+                                                           __builtin_bit_cast(half8_t, fr[NT + j]), acc[i][j], 0, 0, 0);
+    };
+
+    if (S > 0) {
+        for (int p = 0; p < kRing; p++) {
+#pragma unroll
+            for (int t = 0; t < kCopies; t++) copy(t, p);
+            advance();
+        }
+        step_barrier<3 * kCopies>();
+#pragma unroll
+        for (int f = 0; f < NT + MT; f++) read(f, 0, 0, fa);
+    }
+    constexpr int kM = NT * MT;
+    for (int64_t i = 0; i < S; i++) {
+        const int slot = (int)(i & (kRing - 1)), next = (int)((i + 1) & (kRing - 1));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < kM; q++) {
+            mfma(q, fa);
+#pragma unroll
+            for (int f = 0; f < NT + MT; f++)
+                if (f * kM / (2 * (NT + MT)) == q) read(f, slot, 1, fb);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        step_barrier<2 * kCopies>();
+#pragma unroll
+        for (int q = 0; q < kM; q++) {
+            mfma(q, fb);
+#pragma unroll
+            for (int f = 0; f < NT + MT; f++)
+                if (f * kM / (2 * (NT + MT)) == q) read(f, next, 0, fa);
+#pragma unroll
+            for (int t = 0; t < kCopies; t++)
+                if (kM / 2 + t * kM / (2 * kCopies) == q) copy(t, slot);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        advance();
+    }
+
+    // ---- epilogue ----------------------------------------------------------------
+    // every copy has landed and every wave has read its last fragments
+    step_barrier<0>();
+    float* tile = reinterpret_cast<float*>(lds) + wave * 32 * kRowF;
+    constexpr int kCols = EPI == EPI_GATED ? NT * 16 : NT * 32;      // output columns of the wave
+    constexpr int kChunks = kCols / 8;
+    const int64_t N = a.epi.N, M = a.epi.M;
+    const int64_t n0 = EPI == EPI_GATED ? (pn0 + wn * NT) * 16 : (pn0 + wn * NT) * 32;
+    const bool vec = N % 8 == 0;
+#pragma unroll
+    for (int j = 0; j < MT; j++) {
+        const int64_t m0 = (pm0 + wm * MT + j) * 32;
+        const int64_t mine = m0 + (lane & 31);
+        const float back = mine < M ? ldexpf(1.0f, -(int)a.xexp[mine]) : 0.0f;
+        // lane: row lane & 31 of the panel, columns 8 (e / 4) + 4 (lane >> 5) + e % 4
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                floatx4_t t;
+#pragma unroll
+                for (int e = 0; e < 4; e++) t[e] = acc[i][j][4 * q + e] * back;
+                *reinterpret_cast<floatx4_t*>(tile + (lane & 31) * kRowF + i * 32 + 8 * q + 4 * (lane >> 5)) = t;
+            }
+        for (int c0 = 0; c0 < 32 * kChunks; c0 += 64) {
+            const int c = c0 + lane;
+            const int row = c / kChunks, col = c % kChunks * 8;
+            const int64_t m = m0 + row, n = n0 + col;
+            float z[8], z2[8];
+            auto fetch = [&](int at, float (&f)[8]) __attribute__((always_inline)) {
+                const floatx4_t* p = reinterpret_cast<const floatx4_t*>(tile + row * kRowF + at);
+                const floatx4_t lo = p[0], hi = p[1];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    f[e] = lo[e];
+                    f[4 + e] = hi[e];
+                }
+            };
+            if constexpr (EPI == EPI_GATED) {
+                fetch(col / 32 * 64 + col % 32, z);
+                fetch(col / 32 * 64 + 32 + col % 32, z2);
+            } else {
+                fetch(col, z);
+            }
+            if (m >= M) continue;
+            if constexpr (EPI == EPI_PARTIAL) {
+                const int64_t np = a.w_panels * 32;
+                if (n < np) {
+                    floatx4_t* p = reinterpret_cast<floatx4_t*>(a.part + ((int64_t)part * M + m) * np + n);
+                    p[0] = floatx4_t{z[0], z[1], z[2], z[3]};
+                    p[1] = floatx4_t{z[4], z[5], z[6], z[7]};
+                }
+            } else {
+                if (n >= N) continue;
+                if (vec) epilogue8<EPI, true>(a.epi, m, n, z, z2);
+                else epilogue8<EPI, false>(a.epi, m, n, z, z2);
+            }
+        }
+    }
+}
+
+// The parts of a split sum joined in order, then the epilogue: one thread for
+// eight columns of a row.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_tile_join(const TileArgs a) {
+    const int64_t chunks = (a.epi.N + 7) / 8;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= a.epi.M * chunks) return;
+    const int64_t m = id / chunks, n = id % chunks * 8, np = a.w_panels * 32;
+    const int64_t at = EPI == EPI_GATED ? n / 32 * 64 + n % 32 : n;
+    float z[8] = {0, 0, 0, 0, 0, 0, 0, 0}, z2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int p = 0; p < a.parts; p++) {
+        const float* row = a.part + ((int64_t)p * a.epi.M + m) * np + at;
+        auto add = [&](const float* q, float (&f)[8]) __attribute__((always_inline)) {
+            const floatx4_t lo = reinterpret_cast<const floatx4_t*>(q)[0], hi = reinterpret_cast<const floatx4_t*>(q)[1];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                f[e] += lo[e];
+                f[4 + e] += hi[e];
+            }
+        };
+        add(row, z);
+        if constexpr (EPI == EPI_GATED) add(row + 32, z2);
+    }
+    if (a.epi.N % 8 == 0) epilogue8<EPI, true>(a.epi, m, n, z, z2);
+    else epilogue8<EPI, false>(a.epi, m, n, z, z2);
+}
+
+// ---- host ------------------------------------------------------------------------
+
+// Cost of a plan in cycles: rounds of workgroups over the CUs, each a start
+// and, per step, the larger of the MFMAs' time and LDS's.
+static double plan_cost(int nt, int mt, int parts, int64_t w_panels, int64_t x_panels, int64_t steps, int cus) {
+    const int64_t tiles = ((w_panels + 2 * nt - 1) / (2 * nt)) * ((x_panels + 2 * mt - 1) / (2 * mt));
+    const int64_t rounds = (tiles * parts + cus - 1) / cus;
+    const double mfma = 64.0 * nt * mt, lds = 112.0 * (nt + mt);
+    const double step = (mfma > lds ? mfma : lds) + 60.0;
+    const double one = 5000.0 + step * (double)((steps + parts - 1) / parts);
+    // the parts' sums travel to memory and back, and a join is a launch more
+    const double join = parts > 1 ? 6000.0 + 8.0 * parts * (double)(x_panels * w_panels) * 1024.0 / 2000.0 : 0.0;
+    return rounds * one + join;
+}
+
+TilePlan plan_tiles(int nmat, int64_t M, int64_t N, int64_t K) {
+    const int64_t w_panels = (N + 31) / 32 * nmat, x_panels = (M + 31) / 32, steps = image_slices(K) / 2;
+    const int cus = current_cu_count();
+    TilePlan best{4, 4, 1};
+    double least = -1.0;
+    constexpr int kShapes[][2] = {{4, 4}, {4, 2}, {2, 4}, {2, 2}};
+    for (const auto& sh : kShapes)
+        for (int parts = 1; parts <= 16; parts *= 2) {
+            if (parts > 1 && steps / parts < 8) break;
+            const double c = plan_cost(sh[0], sh[1], parts, w_panels, x_panels, steps, cus);
+            if (least < 0.0 || c < least) {
+                least = c;
+                best = TilePlan{sh[0], sh[1], parts};
+            }
+        }
+    return best;
+}
+
+int64_t partial_bytes(const TilePlan& p, int64_t M, int64_t w_panels) {
+    return p.parts > 1 ? (int64_t)p.parts * M * w_panels * 32 * 4 : 0;
+}
+
+template <int NT, int MT>
+static void launch_shape(int epi, const TileArgs& a, unsigned grid, hipStream_t s) {
+    if (epi == EPI_PARTIAL) hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_PARTIAL>), dim3(grid), dim3(256), 0, s, a);
+    else if (epi == EPI_GATED) hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_GATED>), dim3(grid), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_LINEAR>), dim3(grid), dim3(256), 0, s, a);
+}
+
+hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& args, hipStream_t s) {
+    TileArgs a = args;
+    a.parts = p.parts;
+    const int last = nmat == 2 ? EPI_GATED : EPI_LINEAR;
+    const int epi = p.parts > 1 ? EPI_PARTIAL : last;
+    const int64_t tiles =
+        ((a.w_panels + 2 * p.nt - 1) / (2 * p.nt)) * ((a.x_panels + 2 * p.mt - 1) / (2 * p.mt)) * p.parts;
+    if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (p.nt == 4 && p.mt == 4) launch_shape<4, 4>(epi, a, (unsigned)tiles, s);
+    else if (p.nt == 4) launch_shape<4, 2>(epi, a, (unsigned)tiles, s);
+    else if (p.mt == 4) launch_shape<2, 4>(epi, a, (unsigned)tiles, s);
+    else launch_shape<2, 2>(epi, a, (unsigned)tiles, s);
+    if (p.parts > 1) {
+        const int64_t threads = a.epi.M * ((a.epi.N + 7) / 8);
+        if ((threads + 255) / 256 > 0x7FFFFFFF) return hipErrorInvalidValue;
+        const dim3 grid((unsigned)((threads + 255) / 256));
+        if (last == EPI_GATED) hipLaunchKernelGGL((k_tile_join<EPI_GATED>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((k_tile_join<EPI_LINEAR>), grid, dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace q4

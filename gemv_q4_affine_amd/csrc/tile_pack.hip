@@ -1,0 +1,388 @@
+// tile_pack.hip -- the packers of the dense product's operand images
+// (tile_image.hpp): weights dequantised to binary16, by rows or transposed;
+// activations and gradients scaled to binary16 row by row.  All are bound by
+// memory (a quantised matrix read, two bytes a weight written).
+#include "tile_image.hpp"
+
+namespace q4 {
+
+// ---- weights ---------------------------------------------------------------------
+//
+// Dequantised exactly in binary32 ((q - 8) d has 15 bits, q s + b one rounding)
+// and rounded once to binary16.
+
+// Codes as binary32: byte e of w (8-bit), or its low / high nibble.
+template <int E>
+__device__ __forceinline__ float byte_f32(uint32_t w) { return (float)((w >> (8 * E)) & 0xFFu); }
+
+template <int WF>
+struct RowScale {
+    float s, b;
+    __device__ __forceinline__ float operator()(float q) const {
+        return WF == WF_Q4_0 ? (q - 8.0f) * s : __builtin_fmaf(q, s, b);
+    }
+};
+template <int WF>
+__device__ __forceinline__ RowScale<WF> row_scale(const QuantW& w, int64_t n, int64_t blk32, int64_t K) {
+    if constexpr (WF == WF_Q4_0) {
+        return {f16_to_f32(w.s[n * (K / 32) + blk32]), 0.0f};
+    } else {
+        const int64_t g = n * (K / 64) + (blk32 >> 1);
+        return {bf16_to_f32(w.s[g]), bf16_to_f32(w.b[g])};
+    }
+}
+
+// Image of W: lane (row j, half h) of a wave takes whole blocks of 32 weights,
+// block 2 t + h of the row in pass t, and writes each as its four 16-byte
+// pieces; for one piece 32 lanes write 512 contiguous bytes.  A wave does 256
+// weights of a row (a row's 128 contiguous code bytes at 4 bits), four waves a
+// workgroup.
+template <int WF>
+__global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int mats, int N, int64_t K, int64_t slices,
+                                                      int64_t kgroups, uint8_t* __restrict__ img) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 31, h = lane >> 5;
+    const int64_t panel = blockIdx.x / kgroups;
+    const QuantW w = mats == 2 && (panel & 1) ? w1 : w0;
+    int64_t n = panel / mats * 32 + j;
+    n = n < N ? n : N - 1;                   // rows past N: their outputs are never stored
+    const int64_t nb = K / 32, b0 = (blockIdx.x % kgroups * 4 + wave) * 8;
+    constexpr int kWords = WF == WF_AFFINE8 ? 2 : 1;
+    u32x4_t raw[4][kWords];
+    RowScale<WF> sc[4];
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+        int64_t b = b0 + 2 * t + h;
+        b = b < nb ? b : nb - 1;
+        const u32x4_t* q = reinterpret_cast<const u32x4_t*>(w.q + (n * nb + b) * (16 * kWords));
+#pragma unroll
+        for (int e = 0; e < kWords; e++) raw[t][e] = __builtin_nontemporal_load(q + e);
+        sc[t] = row_scale<WF>(w, n, b, K);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+        const int64_t b = b0 + 2 * t + h;
+        if (b >= nb) continue;
+        uint8_t* out = img + (panel * slices + 2 * b) * kUnit + j * 16;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {        // elements 8 c .. 8 c + 7: slice c / 2, half c % 2
+            float f[8];
+            if constexpr (WF == WF_AFFINE8) {
+                const uint32_t lo = raw[t][c >> 1][2 * (c & 1)], hi = raw[t][c >> 1][2 * (c & 1) + 1];
+                f[0] = byte_f32<0>(lo); f[1] = byte_f32<1>(lo); f[2] = byte_f32<2>(lo); f[3] = byte_f32<3>(lo);
+                f[4] = byte_f32<0>(hi); f[5] = byte_f32<1>(hi); f[6] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
+            } else if constexpr (WF == WF_Q4_0) {
+                // elements 0..15 low nibbles, 16..31 high nibbles of bytes 0..15
+                const uint32_t m = 0x0F0F0F0Fu;
+                const uint32_t lo = (c < 2 ? raw[t][0][2 * (c & 1)] : raw[t][0][2 * (c & 1)] >> 4) & m;
+                const uint32_t hi = (c < 2 ? raw[t][0][2 * (c & 1) + 1] : raw[t][0][2 * (c & 1) + 1] >> 4) & m;
+                f[0] = byte_f32<0>(lo); f[1] = byte_f32<1>(lo); f[2] = byte_f32<2>(lo); f[3] = byte_f32<3>(lo);
+                f[4] = byte_f32<0>(hi); f[5] = byte_f32<1>(hi); f[6] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
+            } else {
+                // byte i: elements 2 i (low nibble) and 2 i + 1
+                const uint32_t lo = raw[t][0][c] & 0x0F0F0F0Fu, hi = (raw[t][0][c] >> 4) & 0x0F0F0F0Fu;
+                f[0] = byte_f32<0>(lo); f[2] = byte_f32<1>(lo); f[4] = byte_f32<2>(lo); f[6] = byte_f32<3>(lo);
+                f[1] = byte_f32<0>(hi); f[3] = byte_f32<1>(hi); f[5] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) f[e] = sc[t](f[e]);
+            *reinterpret_cast<u32x4_t*>(out + (c >> 1) * kUnit + (c & 1) * 512) = pack8(DT_F16, f);
+        }
+    }
+}
+
+// Image of W^T (rows k, summed over n; n past N are zeros): a workgroup takes 64
+// rows n by kTileK weights.  A thread loads one 32-bit word of codes from each
+// of eight consecutive rows (a row's words over consecutive lanes: 128
+// contiguous bytes) and holds the codes of 8 n for 8 (4) k: eight (four)
+// 16-byte pieces of the image.  They change places in LDS, where a panel's four
+// units lie as in memory, and leave as whole units.
+template <int WF>
+__global__ __launch_bounds__(256) void k_pack_weights_t(QuantW w0, QuantW w1, int N, int64_t K, int64_t slices,
+                                                        int64_t ktiles, int64_t ntiles, uint8_t* __restrict__ img) {
+    constexpr int kPer = WF == WF_AFFINE8 ? 4 : 8;           // weights of a code word
+    constexpr int kTileK = 32 * kPer;
+    constexpr int kTilePanels = kTileK / 32;
+    constexpr int kPanelB = 4 * kUnit + 16;                  // the 16 spread the panels over the banks
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kTilePanels * kPanelB];
+    const int tid = threadIdx.x, word = tid & 31, o = tid >> 5;       // code word of the tile's row, octet of rows
+    const int64_t kt = blockIdx.x % ktiles, rest = blockIdx.x / ktiles;
+    const int64_t nt = rest % ntiles;
+    const int mat = (int)(rest / ntiles);
+    const QuantW w = mat ? w1 : w0;
+    const int64_t k0 = kt * kTileK + word * kPer;            // this word's first position, in code order
+    const int64_t n0 = nt * 64 + o * 8;
+    constexpr int kWordsPerBlk = 32 / kPer;                  // of a block of 32
+    const int p = word / kWordsPerBlk, wb = word % kWordsPerBlk;
+    const int64_t blk = k0 / 32, nb = K / 32;
+    const bool in_k = blk < nb;
+    uint32_t raw[8];
+    RowScale<WF> sc[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const bool ok = in_k && n0 + i < N;
+        const int64_t n = n0 + i < N ? n0 + i : N - 1, b = in_k ? blk : nb - 1;
+        raw[i] = *reinterpret_cast<const uint32_t*>(w.q + (n * nb + b) * (128 / kPer) + wb * 4);
+        sc[i] = row_scale<WF>(w, n, b, K);
+        if (!ok) {
+            sc[i].s = 0.0f;
+            sc[i].b = 0.0f;
+            raw[i] = 0u;
+        }
+    }
+    uint8_t* base = lds + p * kPanelB + (o >> 1) * kUnit + (o & 1) * 512;
+    auto put = [&](int j, auto code) __attribute__((always_inline)) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] = sc[i](code(raw[i]));
+        *reinterpret_cast<u32x4_t*>(base + j * 16) = pack8(DT_F16, f);
+    };
+    if constexpr (WF == WF_AFFINE8) {
+        put(4 * wb + 0, [](uint32_t v) { return byte_f32<0>(v); });
+        put(4 * wb + 1, [](uint32_t v) { return byte_f32<1>(v); });
+        put(4 * wb + 2, [](uint32_t v) { return byte_f32<2>(v); });
+        put(4 * wb + 3, [](uint32_t v) { return byte_f32<3>(v); });
+    } else {
+        // Q4_0: byte i of word wb holds elements 4 wb + i and 16 + 4 wb + i;
+        // affine: elements 8 wb + 2 i and 8 wb + 2 i + 1
+        constexpr int kStep = WF == WF_Q4_0 ? 1 : 2, kHigh = WF == WF_Q4_0 ? 16 : 1;
+        const int j0 = WF == WF_Q4_0 ? 4 * wb : 8 * wb;
+        put(j0 + 0 * kStep, [](uint32_t v) { return byte_f32<0>(v & 0x0F0F0F0Fu); });
+        put(j0 + 1 * kStep, [](uint32_t v) { return byte_f32<1>(v & 0x0F0F0F0Fu); });
+        put(j0 + 2 * kStep, [](uint32_t v) { return byte_f32<2>(v & 0x0F0F0F0Fu); });
+        put(j0 + 3 * kStep, [](uint32_t v) { return byte_f32<3>(v & 0x0F0F0F0Fu); });
+        put(j0 + 0 * kStep + kHigh, [](uint32_t v) { return byte_f32<0>((v >> 4) & 0x0F0F0F0Fu); });
+        put(j0 + 1 * kStep + kHigh, [](uint32_t v) { return byte_f32<1>((v >> 4) & 0x0F0F0F0Fu); });
+        put(j0 + 2 * kStep + kHigh, [](uint32_t v) { return byte_f32<2>((v >> 4) & 0x0F0F0F0Fu); });
+        put(j0 + 3 * kStep + kHigh, [](uint32_t v) { return byte_f32<3>((v >> 4) & 0x0F0F0F0Fu); });
+    }
+    __syncthreads();
+    const int64_t mat_slices = ((int64_t)N + 31) / 32 * 2;
+#pragma unroll
+    for (int t = 0; t < kTilePanels; t++) {                  // a wave writes one unit of the panel
+        const int64_t panel = kt * kTilePanels + t, sl = nt * 4 + (tid >> 6);
+        if (panel * 32 >= K || sl >= mat_slices) continue;
+        *reinterpret_cast<u32x4_t*>(img + (panel * slices + mat * mat_slices + sl) * kUnit + (tid & 63) * 16) =
+            *reinterpret_cast<const u32x4_t*>(lds + t * kPanelB + tid * 16);
+    }
+}
+
+template <int WF>
+static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, uint8_t* img,
+                                 hipStream_t s) {
+    if (!transposed) {
+        const int64_t kgroups = (K + 1023) / 1024, blocks = (N + 31) / 32 * mats * kgroups;
+        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((k_pack_weights<WF>), dim3((unsigned)blocks), dim3(256), 0, s, w[0], w[mats - 1], mats, (int)N, K,
+                           image_slices(K), kgroups, img);
+    } else {
+        constexpr int kTileK = WF == WF_AFFINE8 ? 128 : 256;
+        const int64_t ktiles = (K + kTileK - 1) / kTileK, ntiles = (N + 63) / 64, blocks = ktiles * ntiles * mats;
+        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        hipLaunchKernelGGL((k_pack_weights_t<WF>), dim3((unsigned)blocks), dim3(256), 0, s, w[0], w[mats - 1], (int)N, K,
+                           image_slices(N) * mats, ktiles, ntiles, img);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, uint8_t* img,
+                               hipStream_t s) {
+    if (wf == WF_Q4_0) return pack_weights_t<WF_Q4_0>(mats, w, N, K, transposed, img, s);
+    if (wf == WF_AFFINE4) return pack_weights_t<WF_AFFINE4>(mats, w, N, K, transposed, img, s);
+    return pack_weights_t<WF_AFFINE8>(mats, w, N, K, transposed, img, s);
+}
+
+// ---- rows of activations and gradients ----------------------------------------------
+//
+// A row is multiplied by the power of two 2^e that brings its largest |value|
+// into [2^14, 2^15) and rounded to binary16: the whole bfloat16 range fits, and
+// values down to 2^-29 of the row's largest keep binary16's 11 bits (bfloat16
+// values: exact).  The product's epilogue takes 2^-e off again.  A workgroup
+// takes eight rows, so that a piece's eight rows are 128 contiguous bytes of
+// the image; it reads them twice, the second time from cache.
+constexpr int kPackThreads = 1024;
+
+__device__ __forceinline__ int row_exponent(float mx) {
+    if (!(mx > 0.0f) || mx > 3.4028234663852886e38f) return 0;          // zero, infinite or NaN
+    const int e = 14 - (__builtin_amdgcn_frexp_expf(mx) - 1);
+    return e < -113 ? -113 : e > 127 ? 127 : e;
+}
+
+// Maximum over the lanes and waves that hold the same row (lane & 7).
+__device__ __forceinline__ float rows_max(float mx, float (*red)[8]) {
+    mx = fmaxf(mx, __shfl_xor(mx, 8, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const int lane = threadIdx.x & 63;
+    if (lane < 8) red[threadIdx.x >> 6][lane] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPackThreads / 64; w++) mx = fmaxf(mx, red[w][lane & 7]);
+    return mx;
+}
+
+__device__ __forceinline__ uint8_t* piece(uint8_t* img, int64_t m, int64_t slices, int64_t c) {
+    return img + (m / 32 * slices + (c >> 1)) * kUnit + (c & 1) * 512 + (m & 31) * 16;
+}
+
+__device__ __forceinline__ float max8(const float (&v)[8], float mx) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) mx = fmaxf(mx, fabsf(v[e]));
+    return mx;
+}
+
+__global__ __launch_bounds__(kPackThreads) void k_pack_rows(const void* __restrict__ x, int dtype, int64_t M, int64_t K,
+                                                            int64_t slices, uint8_t* __restrict__ img,
+                                                            int8_t* __restrict__ xexp) {
+    __shared__ float red[kPackThreads / 64][8];
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 8 + (lane & 7), c0 = (threadIdx.x >> 6) * 8 + (lane >> 3);
+    const int64_t row = (m < M ? m : M - 1) * K, chunks = K / 8;          // K % 32 == 0
+    float v[8], mx = 0.0f;
+    for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+        unpack8(dtype, load8_raw<true>(x, row + c * 8, 8), v);
+        mx = max8(v, mx);
+    }
+    const int e = row_exponent(rows_max(mx, red));
+    const float scale = ldexpf(1.0f, e);
+    if (m < M) {
+        for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+            unpack8(dtype, load8_raw<true>(x, row + c * 8, 8), v);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] *= scale;
+            *reinterpret_cast<u32x4_t*>(piece(img, m, slices, c)) = pack8(DT_F16, v);
+        }
+        if (threadIdx.x < 8) xexp[m] = (int8_t)e;
+    }
+}
+
+hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, uint8_t* img, int8_t* xexp, hipStream_t s) {
+    hipLaunchKernelGGL(k_pack_rows, dim3((unsigned)((M + 7) / 8)), dim3(kPackThreads), 0, s, x, dtype, M, K,
+                       image_slices(K), img, xexp);
+    return hipGetLastError();
+}
+
+// dz of the projections: the same image (the projections' slices follow each
+// other), the dz outputs rounded from the same binary32 values, and the sums of
+// the workgroup's eight rows, joined by k_join_sums in a fixed order.
+template <bool VEC>
+__device__ __forceinline__ void load_dz(const LinearGradArgs& a, int64_t o, int left, float (&dz)[2][8]) {
+    unpack8(DT_BF16, load8_raw<VEC>(a.dy, o, left), dz[0]);
+    if (a.pre[0]) {
+        float g[8];
+        unpack8(DT_BF16, load8_raw<VEC>(a.pre[0], o, left), g);
+        if (a.nmat == 2) {
+            float u[8];
+            unpack8(DT_BF16, load8_raw<VEC>(a.pre[1], o, left), u);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                float slope;
+                const float v = activate<true>(a.act, g[e], slope), dh = dz[0][e];
+                dz[0][e] = dh * u[e] * slope;
+                dz[1][e] = dh * v;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                float slope;
+                activate<true>(a.act, g[e], slope);
+                dz[0][e] *= slope;
+            }
+        }
+    }
+    // past the row's end: zeros in the image, whatever the derivative of zeros is
+    if (left < 8) {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (e >= left) dz[0][e] = dz[1][e] = 0.0f;
+    }
+}
+
+template <bool VEC>
+__global__ __launch_bounds__(kPackThreads) void k_pack_dz(const LinearGradArgs a, int64_t slices, uint8_t* __restrict__ img,
+                                                          int8_t* __restrict__ xexp, float* __restrict__ sums) {
+    __shared__ float red[kPackThreads / 64][8];
+    const int lane = threadIdx.x & 63;
+    const int64_t m = (int64_t)blockIdx.x * 8 + (lane & 7), c0 = (threadIdx.x >> 6) * 8 + (lane >> 3);
+    const int64_t row = (m < a.M ? m : a.M - 1) * a.N, chunks = slices * 2;      // of one projection, padded
+    float dz[2][8], mx = 0.0f;
+    auto left_of = [&](int64_t c) { return (int)(a.N - c * 8 < 8 ? a.N - c * 8 : 8); };
+    for (int64_t c = c0; c * 8 < a.N; c += kPackThreads / 8) {
+        load_dz<VEC>(a, row + c * 8, left_of(c), dz);
+        mx = max8(dz[0], mx);
+        if (a.nmat == 2) mx = max8(dz[1], mx);
+    }
+    const int e = row_exponent(rows_max(mx, red));
+    const float scale = ldexpf(1.0f, e);
+    const bool live = m < a.M;
+    for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+        const int left = left_of(c);
+        load_dz<VEC>(a, row + (left > 0 ? c * 8 : 0), left, dz);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (i >= a.nmat) break;
+            float v[8];
+#pragma unroll
+            for (int t = 0; t < 8; t++) v[t] = dz[i][t];
+            if (live) {
+                if (a.dz[i] && left > 0) store8<VEC>(a.dz[i], row + c * 8, left, pack8(DT_BF16, v));
+                float sv[8];
+#pragma unroll
+                for (int t = 0; t < 8; t++) sv[t] = v[t] * scale;
+                *reinterpret_cast<u32x4_t*>(piece(img, m, slices * a.nmat, c + i * chunks)) = pack8(DT_F16, sv);
+            }
+            if (a.dbias[i]) {
+#pragma unroll
+                for (int t = 0; t < 8; t++) {
+                    float q = live ? v[t] : 0.0f;
+                    q += __shfl_xor(q, 1, 64);
+                    q += __shfl_xor(q, 2, 64);
+                    q += __shfl_xor(q, 4, 64);
+                    v[t] = q;
+                }
+                // lane r of the eight stores column c * 8 + r
+                float mine = v[0];
+#pragma unroll
+                for (int t = 1; t < 8; t++) mine = (lane & 7) == t ? v[t] : mine;
+                if ((lane & 7) < left) sums[((int64_t)blockIdx.x * a.nmat + i) * a.N + c * 8 + (lane & 7)] = mine;
+            }
+        }
+    }
+    if (threadIdx.x < 8 && live) xexp[m] = (int8_t)e;
+}
+
+// Columns of the sums of row groups, in order: a workgroup takes 64 columns of a
+// projection, its four waves a quarter of the groups each.
+__global__ __launch_bounds__(256) void k_join_sums(const float* __restrict__ sums, int64_t groups, int nmat, int64_t N,
+                                                   float* __restrict__ out0, float* __restrict__ out1) {
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.y;
+    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+    float* out = i ? out1 : out0;
+    if (!out) return;
+    const int64_t g0 = groups * wave / 4, g1 = groups * (wave + 1) / 4;
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n < N) {
+        int64_t g = g0;
+        for (; g + 4 <= g1; g += 4)
+#pragma unroll
+            for (int e = 0; e < 4; e++) t[e] += sums[((g + e) * nmat + i) * N + n];
+        for (; g < g1; g++) t[0] += sums[(g * nmat + i) * N + n];
+    }
+    red[wave][lane] = (t[0] + t[1]) + (t[2] + t[3]);
+    __syncthreads();
+    if (wave == 0 && n < N) out[n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+}
+
+int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N) { return (M + 7) / 8 * nmat * N * 4; }
+
+hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s) {
+    const int64_t groups = (a.M + 7) / 8;
+    auto k = a.N % 8 == 0 ? k_pack_dz<true> : k_pack_dz<false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(kPackThreads), 0, s, a, image_slices(a.N), img, xexp, sums);
+    if (a.dbias[0] || a.dbias[1])
+        hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(256), 0, s, sums, groups, a.nmat,
+                           a.N, a.dbias[0], a.dbias[1]);
+    return hipGetLastError();
+}
+
+}  // namespace q4
