@@ -14,6 +14,8 @@
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
+// N and K: a panel of 32 rows of an operand image stays below 2^32 bytes
+constexpr int64_t kMaxSum = int64_t(1) << 25;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -40,7 +42,7 @@ int format_wf(int fmt) {
 
 int check_product(int fmt, int act, int64_t M, int64_t N, int64_t K) {
     if (!fmt_ok(fmt) || !act_ok(act)) return Q4_ERR_ARG;
-    if (M < 0 || N < 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return Q4_ERR_SHAPE;
+    if (M < 0 || N < 0 || K <= 0 || M > kMaxDim || N > kMaxSum || K > kMaxSum) return Q4_ERR_SHAPE;
     if (K % (fmt == Q4_FMT_Q4_0 ? 32 : 64) != 0) return Q4_ERR_SHAPE;
     return Q4_OK;
 }

@@ -11,15 +11,22 @@
 // of the about 110 that LDS moves; 8 waves of 4 x 2 would read 96 KiB.
 //
 // The sum runs in steps of two slices through a ring of four LDS slots that
-// direct-to-LDS copies fill up to four steps ahead.  In a step:
-//   slice 0: its MFMAs, and between the first ones the reads of slice 1;
-//   wait for the copies of the next step (two later ones stay in flight), and
-//   meet at the barrier: every wave has read this step, its slot is free;
-//   slice 1: its MFMAs, the reads of the next step's slice 0, and between the
-//   last ones the copies of the step after next but two, into the free slot.
-// One barrier per 1024 MFMA cycles; no read waits on a copy it does not need.
-// The order is written out and fenced: left alone, the compiler groups the
-// reads and copies and the matrix pipe runs dry behind them.
+// direct-to-LDS copies fill three to four steps ahead.  A step is T = 2 NT MT
+// MFMAs with one barrier before MFMA 3 T / 4: by then this wave has read all of
+// the step (its slot is free for the step after next but two) and waits until
+// the next step has landed (two later ones stay in flight).  Reads stand at
+// least six MFMAs before their use and copies are spread over the whole step:
+// four waves in step that read one fragment per MFMA ask for all that LDS
+// moves, and a burst of copies fills the address pipe; both held the matrix
+// pipe (gated, M = 2048, N = 12288, K = 4096: 352 us with reads and copies
+// bunched, 340 spread).  The order is written out and fenced: left alone, the
+// compiler groups them again.
+//
+// What bounds it: power.  A loop of nothing but these MFMAs on random operands
+// reaches 1.67 PFLOP/s (1.35 on 16x16x32 MFMAs), the clock then at 1.6 of 2.4
+// GHz; this kernel 1.37 at K = 12288, M = 4096, N = 4096 (300 us, clock 1.67
+// GHz, matrix pipe 0.77 busy).  Without the copies it takes 266 us, without the
+// barriers 299.
 //
 // The epilogue passes the accumulators through LDS, 32 rows at a time, so that
 // bias, residual and outputs move as whole rows of 16 bytes a lane.
@@ -70,7 +77,7 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     // ---- copies: unit t of this wave is slice (wave & 1) of panel (wave >> 1) + 2 t ----
     const int64_t steps_all = a.slices / 2;
     const int64_t s0 = steps_all * part / a.parts;
-    const int64_t S = steps_all * (part + 1) / a.parts - s0;
+    const int S = (int)(steps_all * (part + 1) / a.parts - s0);
     const uint8_t* src[kCopies];
 #pragma unroll
     for (int t = 0; t < kCopies; t++) {
@@ -82,18 +89,16 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     }
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds) +
                           (uint32_t)((wave >> 1) * 2 + (wave & 1)) * kUnit;
-    const uint32_t voff = (uint32_t)lane * 16;
     // copy t of the next step to request, into slot; after the last step the
     // last one is copied again (and never read), so that a wait counts alike
-    int64_t ahead = 0;                                       // step the pointers stand at
+    uint32_t voff = (uint32_t)lane * 16;                     // in the panel: below 2^32 for sums of at most 2^26 terms
+    int ahead = 0;                                           // step it stands at
     auto copy = [&](int t, int slot) __attribute__((always_inline)) {
         copy_unit(src[t], voff, lds0 + (uint32_t)slot * kSlot + (uint32_t)t * 4 * kUnit);
     };
     auto advance = [&]() __attribute__((always_inline)) {
         ahead++;
-        const int64_t by = ahead < S ? 2 * kUnit : 0;
-#pragma unroll
-        for (int t = 0; t < kCopies; t++) src[t] += by;
+        voff += ahead < S ? 2 * kUnit : 0;
     };
 
     floatx16_t acc[NT][MT];
@@ -116,41 +121,60 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
                                                            __builtin_bit_cast(half8_t, fr[NT + j]), acc[i][j], 0, 0, 0);
     };
 
+    // ---- the schedule of a step: T MFMAs, the reads and copies between them ----
+    // MFMA q of a slice uses weights fragment q / MT and x fragment q % MT, so a
+    // slice's fragments are needed in the order W0, X0 .. , W1, W2 ..
+    constexpr int kM = NT * MT, T = 2 * kM;
+    constexpr int kFrags = NT + MT;
+    constexpr int B = 3 * T / 4;                            // the barrier stands before MFMA B
+    constexpr int kEarly = MT + 2;                          // W0, X*, W1 of slice 0: read after the step before's barrier
+    constexpr int kLate = 2 * kFrags - kEarly;              // the rest, and slice 1: read before this step's barrier
+    constexpr int kLead = T / 4 < 6 ? T / 4 : 6;            // MFMAs between the last of them and the barrier
+    constexpr int kUnwrapped = (T - B - 1 + (T / kCopies) - 1) / (T / kCopies);   // copies from the barrier to the step's end
+    static_assert(T >= kCopies, "at most one copy after an MFMA");
+    auto frag_at = [](int r) constexpr { return r == 0 ? 0 : r <= MT ? NT + r - 1 : r - MT; };
+
     if (S > 0) {
-        for (int p = 0; p < kRing; p++) {
+        for (int p = 0; p < kRing - 1; p++) {
 #pragma unroll
             for (int t = 0; t < kCopies; t++) copy(t, p);
             advance();
         }
-        step_barrier<3 * kCopies>();
 #pragma unroll
-        for (int f = 0; f < NT + MT; f++) read(f, 0, 0, fa);
+        for (int t = 0; t < kUnwrapped; t++) copy(t, kRing - 1);
+        step_barrier<2 * kCopies + kUnwrapped>();
+#pragma unroll
+        for (int r = 0; r < kEarly; r++) read(frag_at(r), 0, 0, fa);
     }
-    constexpr int kM = NT * MT;
-    for (int64_t i = 0; i < S; i++) {
-        const int slot = (int)(i & (kRing - 1)), next = (int)((i + 1) & (kRing - 1));
+    for (int i = 0; i < S; i++) {
+        const int slot = i & (kRing - 1), next = (i + 1) & (kRing - 1), before = (i + 3) & (kRing - 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < kM; q++) {
-            mfma(q, fa);
+        for (int q = 0; q < T; q++) {
+            if (q == B) {
+                advance();
+                step_barrier<2 * kCopies>();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (q < kM) mfma(q, fa);
+            else mfma(q - kM, fb);
 #pragma unroll
-            for (int f = 0; f < NT + MT; f++)
-                if (f * kM / (2 * (NT + MT)) == q) read(f, slot, 1, fb);
+            for (int r = 0; r < kLate; r++)
+                if (r * (B - kLead) / kLate == q) {
+                    if (r < kFrags - kEarly) read(frag_at(r + kEarly), slot, 0, fa);
+                    else read(frag_at(r - (kFrags - kEarly)), slot, 1, fb);
+                }
+#pragma unroll
+            for (int r = 0; r < kEarly; r++)
+                if (B + r * (T - B) / kEarly == q) read(frag_at(r), next, 0, fa);
+#pragma unroll
+            for (int t = 0; t < kCopies; t++) {
+                const int at = B + 1 + t * (T / kCopies);
+                if (at < T && at == q) copy(t, slot);
+                if (at >= T && at - T == q) copy(t, before);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
-        step_barrier<2 * kCopies>();
-#pragma unroll
-        for (int q = 0; q < kM; q++) {
-            mfma(q, fb);
-#pragma unroll
-            for (int f = 0; f < NT + MT; f++)
-                if (f * kM / (2 * (NT + MT)) == q) read(f, next, 0, fa);
-#pragma unroll
-            for (int t = 0; t < kCopies; t++)
-                if (kM / 2 + t * kM / (2 * kCopies) == q) copy(t, slot);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        advance();
     }
 
     // ---- epilogue ----------------------------------------------------------------

@@ -57,7 +57,8 @@ extern "C" {
  *   bias     : device, [N] of dtype, or NULL
  *   residual : device, [M][N] of dtype, or NULL; may be y itself
  *   pre      : device out, [M][N] of dtype: z (for the backward pass), or NULL
- *   K % 32 == 0 (Q4_0) or K % 64 == 0 (affine).
+ *   K % 32 == 0 (Q4_0) or K % 64 == 0 (affine); N, K <= 2^25, M <= 2^30 (here
+ *   and in the other products).
  *   workspace: q4_linear_workspace_size(fmt, M, N, K) bytes (0: may be NULL),
  *              else Q4_ERR_WORKSPACE.  Calls sharing it must not overlap.
  */
