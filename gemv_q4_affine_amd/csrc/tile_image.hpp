@@ -73,12 +73,16 @@ hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, f
 
 // ---- eight values at a time ----------------------------------------------------
 
-// Eight consecutive 16-bit values, `left` of them inside the tensor (>= 8:
-// one 16-byte load; VEC promises alignment), the others zero.
+// Eight consecutive 16-bit values, `left` of them inside the tensor (>= 8: one
+// 16-byte access), the others zero.  VEC: rows are 16-byte aligned and `left`
+// is 8 or at most 0; else an access is aligned to its elements only, which
+// global memory takes too.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
 template <bool VEC>
 __device__ __forceinline__ u32x4_t load8_raw(const void* p, int64_t i, int left) {
     const uint16_t* q = static_cast<const uint16_t*>(p) + i;
     if (VEC) return left > 0 ? *reinterpret_cast<const u32x4_t*>(q) : u32x4_t{0u, 0u, 0u, 0u};
+    if (left >= 8) return *reinterpret_cast<const u32x4_any_t*>(q);
     u32x4_t r = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; e++)
@@ -114,6 +118,10 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int left, const u32x4
     uint16_t* q = static_cast<uint16_t*>(p) + i;
     if (VEC) {
         if (left > 0) *reinterpret_cast<u32x4_t*>(q) = r;
+        return;
+    }
+    if (left >= 8) {
+        *reinterpret_cast<u32x4_any_t*>(q) = r;
         return;
     }
 #pragma unroll
