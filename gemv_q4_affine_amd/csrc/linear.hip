@@ -1,5 +1,6 @@
 // linear.hip -- q4_linear, q4_gated and their gradients: which kernels a call
 // takes and how it divides its workspace.
+#include "linear_few.hpp"
 #include "tile_image.hpp"
 
 namespace q4 {
@@ -50,10 +51,12 @@ TileArgs tile_args(const Layout& l, uint8_t* ws) {
 }  // namespace
 
 int64_t linear_workspace_bytes(int, int nmat, int64_t M, int64_t N, int64_t K) {
-    return forward_layout(nmat, M, N, K).total;
+    return M <= kFewMaxM ? 0 : forward_layout(nmat, M, N, K).total;
 }
 
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
+    if (a.M <= kFewMaxM)
+        return a.wf == WF_Q4_0 ? launch_few_q4_0(a, s) : a.wf == WF_AFFINE4 ? launch_few_affine4(a, s) : launch_few_affine8(a, s);
     const Layout l = forward_layout(a.nmat, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, ws, s);

@@ -1,0 +1,8 @@
+// linear_few_q4_0.hip -- the few-row product (linear_few.hpp) on its format.
+#include "linear_few.hpp"
+
+namespace q4 {
+
+hipError_t launch_few_q4_0(const LinearArgs& a, hipStream_t s) { return few_format<WF_Q4_0>(a, s); }
+
+}  // namespace q4
