@@ -89,6 +89,15 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
 int64_t norm_grad_workspace_bytes(int64_t M, int64_t D, int64_t gate_rows);
 hipError_t launch_block_norm_grad(const NormGradArgs& a, void* workspace, hipStream_t s);
 
+// One direct-to-LDS copy: lane l's 16 bytes at src + voff land at LDS address
+// m0 + 16 l.  Inline assembly, so that the compiler does not take it for an LDS
+// store and wait for every copy in flight before each read; the kernels' own
+// waits order the copies with the reads.  No register receives data.
+__device__ __forceinline__ void copy_unit(const uint8_t* src, uint32_t voff, uint32_t m0) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(src), "s"(m0)
+                 : "memory", "m0");
+}
+
 // ---- typed element access ----------------------------------------------------
 
 __device__ __forceinline__ float load_elem(const void* p, int dt, int64_t i) {

@@ -13,23 +13,37 @@
 // are q - 8 and q themselves.  Products are exact, sums binary32: the result
 // differs from the exact one by binary32 summation and the output's rounding.
 //
-// Layout.  A lane (j = lane & 15, g = lane >> 4) loads 16 bytes of row j of a
-// column tile: 16 rows of 64 contiguous bytes an instruction, 128 weights of a
-// row at 4 bits.  At 4 bits that is block 4 c + g whole, where the MFMA of block
-// t wants dword g of block 4 c + t: a 4 x 4 transposition over the four g, four
-// lane swaps (v_permlane32_swap, v_permlane16_swap).  At 8 bits the MFMA's k
-// order follows the load instead (a group has one scale).  The x fragments
-// follow the same order and come from L2: every workgroup reads all of x, so a
-// workgroup takes NT column tiles.
+// Layout.  The MFMA wants 16 rows of W across neighbouring lanes; memory wants
+// neighbouring lanes on one row: read in the MFMA's order a load touches 64
+// separate pieces (12 us for 28 MB, its address processing the bound).  So the
+// codes go through LDS: a step is 128 bytes of each of a tile's 16 rows (256
+// weights at 4 bits, 128 at 8), two direct-to-LDS copies of 8 rows by 128
+// contiguous bytes, pieces of 16 bytes placed by an XOR with the row so that a
+// wave's reads (lane j = lane & 15, g = lane >> 4: row j, pieces g and 4 + g) meet
+// no bank twice.  The scales of a step are 16 bytes a row, loaded by one lane a
+// row and passed through LDS too; x lies in LDS in the fragments' order, a slice
+// of K at a time.
 //
-// The waves of a workgroup split K by chunks of 128, two chunks in flight each,
-// and add their sums through LDS in wave order (deterministic).  For q4_gated
-// the tiles come in pairs, gate and up of the same 16 columns.
+// At 4 bits a lane then holds block 4 c + g whole, where the MFMA of block t
+// wants dword g of block 4 c + t: a 4 x 4 transposition over the four g, four
+// lane swaps (v_permlane32_swap, v_permlane16_swap).  Up to four rows (DIAG) it
+// falls away: row 4 m + b of the MFMA's A operand holds x of row m in the lanes
+// g = b only, zeros elsewhere, so the four MFMAs of a chunk sum dwords 0 .. 3 of
+// every lane's own block and row 4 m + b of the result is the whole sum of block
+// b: four scaled additions a chunk and column instead of sixteen.  At 8 bits the
+// MFMA's k order follows the load (a group has one scale).
 //
-// Bound: memory at 1 to 16 rows (each weight byte is read once).
+// The waves of a workgroup take steps in turn, each its next one in flight while
+// it multiplies, and add their sums through LDS in wave order (deterministic).
+// For q4_gated the tiles come in pairs, gate and up of the same 16 columns.
+//
+// Bound: memory at 1 to 16 rows (each weight byte is read once).  Measured, Q4_0,
+// N = 12288, K = 4096: one row 9.5 us (28.3 MB; with no loads at all 4.4), 16
+// rows 14.6, 32 rows 21.5; the gated pair 17.6, 22.6 and 41.
 #pragma once
 
 #include "block_common.hpp"
+#include "gemm_common.hpp"
 
 namespace q4 {
 
@@ -104,122 +118,131 @@ __device__ __forceinline__ u32x4_t bytes8(uint32_t lo, uint32_t hi) {
     return r;
 }
 
-// A chunk of 128 k of one column tile: codes and scales.
-template <int WF>
-struct ChunkW {
-    u32x4_t q[WF == WF_AFFINE8 ? 2 : 1];
-    u32x2_t s;      // Q4_0: d of the four blocks; affine: s and b of the two groups
-};
-
 }  // namespace few
 
-constexpr int kFewMaxM = 64;
+constexpr int kFewMaxM = 32;
 
-template <int WF, int XDT, int MT, int NT, bool GATED>
-__global__ __launch_bounds__(NT * MT <= 3 ? 1024 : 512) void k_linear_few(const LinearArgs a) {
+// Waves and LDS of a variant.  Up to four rows eight waves share a CU's LDS
+// (their steps are what is in flight); with more rows x takes its place.
+template <int MT, bool DIAG> constexpr int few_waves() { return DIAG ? 8 : 4; }
+constexpr int kFewX = 32 << 10;              // x
+
+template <int WF, int XDT, int MT, int NT, bool GATED, bool DIAG>
+__global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const LinearArgs a, int x_shift) {
     using namespace few;
-    constexpr int kMaxWaves = NT * MT <= 3 ? 16 : 8;
-    constexpr int kTile = MT * 16 * 16;
-    __shared__ float red[kMaxWaves * NT * kTile];
+    static_assert(!DIAG || MT == 1, "a form for few rows");
+    constexpr bool kBlocks = DIAG && WF != WF_AFFINE8;       // the block-diagonal x (see above)
+    constexpr int kMaxWaves = few_waves<MT, DIAG>(), kX = kFewX;
+    constexpr int kTile = DIAG ? 4 * 16 : MT * 16 * 16;
+    constexpr int kStepB = 2048, kScaleB = 256;              // codes and scales of a tile and step
+    constexpr int kStep = WF == WF_AFFINE8 ? 128 : 256;      // weights of a row and step
+    constexpr int kRing = kMaxWaves * NT * kStepB, kScales = kMaxWaves * NT * kScaleB;
+    static_assert(kMaxWaves * NT * kTile * 4 <= kRing, "the sums fit where the codes were");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing + kScales + kX + 64];
+    uint8_t* xs = lds + kRing + kScales;
+    float* red = reinterpret_cast<float*>(lds);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
+    const int waves = blockDim.x >> 6, x_rows = 1 << x_shift;
     const int j = lane & 15, g = lane >> 4;
     const int K = (int)a.K, N = (int)a.N, M = (int)a.M;
-    const int nb = K / 32, chunks = (K + 127) / 128;
+    const int nb = K / 32, steps = (K + kStep - 1) / kStep;
     constexpr int kCols = GATED ? NT / 2 : NT;              // column tiles of 16 outputs
     const int n0 = (int)blockIdx.x * kCols * 16;
 
-    // each tile's first row (scalar) and this lane's row in it; rows past N
-    // repeat the last one and are never stored
-    const uint8_t* wq[NT];
-    const uint16_t* ws[NT];
-    const uint16_t* wb[NT];
-    uint32_t row[NT];
-    const int64_t row_q = WF == WF_AFFINE8 ? K : K / 2, row_s = WF == WF_Q4_0 ? nb : K / 64;
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-        const QuantW& w = a.w[GATED ? t & 1 : 0];
-        int first = n0 + (GATED ? t >> 1 : t) * 16;
-        first = first < N ? first : N - 1;
-        const int in = N - 1 - first;
-        row[t] = (uint32_t)(j < in ? j : in);
-        wq[t] = w.q + first * row_q;
-        ws[t] = w.s + first * row_s;
-        wb[t] = WF == WF_Q4_0 ? nullptr : w.b + first * row_s;
-    }
-    const uint8_t* xr[MT];
-    uint32_t xrow[MT];
-#pragma unroll
-    for (int i = 0; i < MT; i++) {
-        int first = i * 16;
-        first = first < M ? first : M - 1;
-        const int in = M - 1 - first;
-        xrow[i] = (uint32_t)(j < in ? j : in) * (uint32_t)K * 2u;
-        xr[i] = static_cast<const uint8_t*>(a.x) + (int64_t)first * K * 2;
-    }
-
-    struct Stage {
-        ChunkW<WF> w[NT];
-        u32x4_t x[MT][4];       // fragments of the four MFMAs of the chunk
+    // ---- a step's loads.  Tile t, row i of it; rows past N repeat the last one
+    // (never stored), pieces past the row's end its last (x is zero there) ----
+    const uint32_t row_q = (uint32_t)(WF == WF_AFFINE8 ? K : K / 2), row_s = (uint32_t)(WF == WF_Q4_0 ? nb : K / 64);
+    auto tile_first = [&](int t) __attribute__((always_inline)) {
+        const int first = n0 + (GATED ? t >> 1 : t) * 16;
+        return first < N ? first : N - 1;
     };
-    auto load = [&](int c, Stage& st) __attribute__((always_inline)) {
-        const bool whole = (c + 1) * 4 <= nb;                // the last chunk may be short
+    auto tile_w = [&](int t) -> const QuantW& { return a.w[GATED ? t & 1 : 0]; };
+    uint32_t copy_row[2];                                    // this lane's rows in the two copies
+#pragma unroll
+    for (int h = 0; h < 2; h++) copy_row[h] = (uint32_t)(8 * h + (lane >> 3));
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds) +
+                          (uint32_t)wave * NT * kStepB;
+    constexpr int kSL = (NT + 3) / 4;                        // scale loads: lane = tile * 16 + row
+    u32x4_t sc[kSL];
+    auto request = [&](int step) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NT; t++) {
-            if constexpr (WF == WF_AFFINE8) {
+            const int first = tile_first(t), in = N - 1 - first;
+            const uint8_t* base = tile_w(t).q + (int64_t)first * row_q;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    int grp = 2 * c + h;
-                    grp = grp < K / 64 ? grp : K / 64 - 1;
-                    st.w[t].q[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
-                        wq[t] + (row[t] * (uint32_t)K + (uint32_t)grp * 64u + (uint32_t)g * 16u)));
-                }
-            } else {
-                int b = 4 * c + g;
-                b = b < nb ? b : nb - 1;
-                st.w[t].q[0] = __builtin_nontemporal_load(
-                    reinterpret_cast<const u32x4_t*>(wq[t] + (row[t] * (uint32_t)(K / 2) + (uint32_t)b * 16u)));
-            }
-            if constexpr (WF == WF_Q4_0) {
-                const uint16_t* p = ws[t] + row[t] * (uint32_t)nb;
-                if (whole) {
-                    st.w[t].s = *reinterpret_cast<const u32x2_u*>(p + 4 * c);
-                } else {
-                    uint32_t d[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) d[e] = p[4 * c + e < nb ? 4 * c + e : nb - 1];
-                    st.w[t].s = u32x2_t{d[0] | d[1] << 16, d[2] | d[3] << 16};
-                }
-            } else {
-                const uint32_t at = row[t] * (uint32_t)(K / 64) + 2 * c;
-                if (whole) {
-                    st.w[t].s = u32x2_t{*reinterpret_cast<const u32_u*>(ws[t] + at), *reinterpret_cast<const u32_u*>(wb[t] + at)};
-                } else {
-                    st.w[t].s = u32x2_t{ws[t][at], wb[t][at]};
-                }
+            for (int h = 0; h < 2; h++) {
+                const uint32_t row = copy_row[h] < (uint32_t)in ? copy_row[h] : (uint32_t)in;
+                const uint32_t p = (uint32_t)step * 8u + ((uint32_t)(lane & 7) ^ (copy_row[h] & 7u)), last = row_q / 16 - 1;
+                copy_unit(base, row * row_q + (p < last ? p : last) * 16u, lds0 + t * kStepB + h * 1024);
             }
         }
 #pragma unroll
-        for (int i = 0; i < MT; i++)
-#pragma unroll
-            for (int t = 0; t < 4; t++) {
-                // a block past K is read at the row's last block and zeroed
-                const int b = 4 * c + t, bc = b < nb ? b : nb - 1;
-                const uint8_t* p = xr[i] + (xrow[i] + (uint32_t)(WF == WF_AFFINE8 ? (bc & ~1) : bc) * 64u);
-                u32x4_t v;
+        for (int e = 0; e < kSL; e++) {
+            int t = e * 4 + g;
+            t = t < NT ? t : NT - 1;
+            const QuantW& w = GATED ? a.w[t & 1] : a.w[0];
+            int n = n0 + (GATED ? t >> 1 : t) * 16 + j;
+            n = n < N ? n : N - 1;
+            const int64_t at = (int64_t)n * row_s;
+            constexpr int kPer = WF == WF_Q4_0 ? 8 : kStep / 64;        // scales of a row and step
+            const int s0 = step * kPer;
+            if (s0 + kPer <= (int)row_s) {
                 if constexpr (WF == WF_Q4_0) {
-                    const u32x2_t lo = *reinterpret_cast<const u32x2_t*>(p + 8 * g);
-                    const u32x2_t hi = *reinterpret_cast<const u32x2_t*>(p + 32 + 8 * g);
-                    v = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+                    sc[e] = *reinterpret_cast<const u32x4_u*>(w.s + at + s0);
                 } else if constexpr (WF == WF_AFFINE4) {
-                    v = *reinterpret_cast<const u32x4_t*>(p + 16 * g);
+                    const u32x2_t s = *reinterpret_cast<const u32x2_u*>(w.s + at + s0), b = *reinterpret_cast<const u32x2_u*>(w.b + at + s0);
+                    sc[e] = u32x4_t{s[0], s[1], b[0], b[1]};
                 } else {
-                    v = *reinterpret_cast<const u32x4_t*>(p + 32 * g + 16 * (bc & 1));
+                    sc[e] = u32x4_t{*reinterpret_cast<const u32_u*>(w.s + at + s0), 0u, *reinterpret_cast<const u32_u*>(w.b + at + s0), 0u};
                 }
-                if (b >= nb) v = u32x4_t{0u, 0u, 0u, 0u};
-                st.x[i][t] = v;
+            } else {
+                // the last step of a K that is no multiple of it: one by one, zeros past the end
+                u32x4_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int i = 0; i < kPer; i++)
+                    if (s0 + i < (int)row_s) {
+                        v[i >> 1] |= (uint32_t)w.s[at + s0 + i] << (16 * (i & 1));
+                        if constexpr (WF != WF_Q4_0) v[2 + (i >> 1)] |= (uint32_t)w.b[at + s0 + i] << (16 * (i & 1));
+                    }
+                sc[e] = v;
             }
+        }
     };
+
+    // ---- x in LDS: [chunk of 128 k][MFMA][row][g][16 bytes], blocks past K zeros.
+    // Piece u of that order, of chunk c: its load, and its place. ----
+    auto x_piece = [&](int c, int u) __attribute__((always_inline)) {
+        const uint16_t* x = static_cast<const uint16_t*>(a.x);
+        const int gg = u & 3, m = (u >> 2) & (x_rows - 1), b = 4 * c + ((u >> (2 + x_shift)) & 3);     // block of 32
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (b < nb) {
+            const uint16_t* p = x + (int64_t)(m < M ? m : M - 1) * K;
+            if constexpr (WF == WF_Q4_0) {
+                // elements 4 g .. + 3 and 16 + 4 g .. + 3
+                const u32x2_t lo = *reinterpret_cast<const u32x2_t*>(p + b * 32 + 4 * gg);
+                const u32x2_t hi = *reinterpret_cast<const u32x2_t*>(p + b * 32 + 16 + 4 * gg);
+                v = u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+            } else if constexpr (WF == WF_AFFINE4) {
+                v = *reinterpret_cast<const u32x4_t*>(p + b * 32 + 8 * gg);
+            } else {
+                v = *reinterpret_cast<const u32x4_t*>(p + (b & ~1) * 32 + 16 * gg + 8 * (b & 1));
+            }
+        }
+        return v;
+    };
+    auto x_put = [&](int u, const u32x4_t& v) __attribute__((always_inline)) {
+        u32x4_t o = v;
+        if constexpr (WF == WF_Q4_0)          // nibble pairs (0, 2), (1, 3) of either half
+            o = u32x4_t{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[1], v[0], 0x07060302u),
+                        __builtin_amdgcn_perm(v[3], v[2], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
+        if constexpr (WF == WF_AFFINE4)       // byte i holds elements 2 i and 2 i + 1: pairs (0, 4), (2, 6), (1, 5), (3, 7)
+            o = u32x4_t{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x05040100u),
+                        __builtin_amdgcn_perm(v[2], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+        *reinterpret_cast<u32x4_t*>(xs + u * 16) = o;
+    };
+    int xat[MT];                                             // this lane's piece of an MFMA's x
+#pragma unroll
+    for (int i = 0; i < MT; i++) xat[i] = ((i * 16 + j < x_rows ? i * 16 + j : x_rows - 1) * 4 + g) * 16;
 
     floatx4_t acc[MT][NT];
 #pragma unroll
@@ -231,38 +254,73 @@ __global__ __launch_bounds__(NT * MT <= 3 ? 1024 : 512) void k_linear_few(const 
     const floatx4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
     auto splat = [](uint32_t v) { return u32x4_t{v, v, v, v}; };
 
-    auto compute = [&](Stage& st) __attribute__((always_inline)) {
+    // kBlocks: this lane's row of A is 4 m + b; its x, or the zeros after the slice
+    const bool diag = (j & 3) == g && (j >> 2) < x_rows;
+    const int diag_at = ((j & 3) * x_rows + (j >> 2)) * 64;
+    if (threadIdx.x < 16) reinterpret_cast<uint32_t*>(xs + kX)[threadIdx.x] = 0u;
+
+    // A chunk of 128 k: codes q (8 bits: two pieces) and scales of every tile, x
+    // chunk `local` of the slice in LDS.  Scale e of the chunk (of its blocks at
+    // Q4_0, of its groups else) and bias e.
+    struct Codes {
+        u32x4_t q[WF == WF_AFFINE8 ? 2 : 1];
+        uint32_t s[2];
+    };
+    auto scale = [](const Codes& c, int e) __attribute__((always_inline)) {
+        if constexpr (WF == WF_Q4_0) return f16_to_f32((c.s[e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
+        else return bf16_to_f32((c.s[0] >> (16 * e)) & 0xFFFFu);
+    };
+    auto bias = [](const Codes& c, int e) __attribute__((always_inline)) { return bf16_to_f32((c.s[1] >> (16 * e)) & 0xFFFFu); };
+    auto compute = [&](Codes (&w)[NT], int local) __attribute__((always_inline)) {
+        u32x4_t x[MT][4];
+        if constexpr (kBlocks) {
+            const uint8_t* p = diag ? xs + local * 4 * x_rows * 64 + diag_at : xs + kX;
+#pragma unroll
+            for (int r = 0; r < 4; r++) x[0][r] = *reinterpret_cast<const u32x4_t*>(p + r * 16);
+            // Q4_0: codes less 8; affine: the sums of x for the group's bias too
+            constexpr bool kOffset = XDT == DT_BF16;
+            const uint32_t one = WF == WF_Q4_0 ? 0xC308C308u : kOffset ? 0xC300C300u : 0x3C003C00u;
+            floatx4_t cs = zero;
+            if (kOffset || WF == WF_AFFINE4) {
+#pragma unroll
+                for (int r = 0; r < 4; r++) cs = mfma16<XDT>(x[0][r], splat(one), cs);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                floatx4_t v = kOffset ? cs : zero;
+#pragma unroll
+                for (int r = 0; r < 4; r++) v = mfma16<XDT>(x[0][r], nibbles<XDT, WF == WF_Q4_0 ? 8 : 0>(w[n].q[0][r], mask), v);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    if constexpr (WF == WF_Q4_0) acc[0][n][e] = fmaf(scale(w[n], e), v[e], acc[0][n][e]);
+                    else
+                        acc[0][n][e] = fmaf(bias(w[n], e >> 1) * (kOffset ? -0.0078125f : 1.0f), cs[e],
+                                            fmaf(scale(w[n], e >> 1), v[e], acc[0][n][e]));
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < MT; i++)
 #pragma unroll
-            for (int t = 0; t < 4; t++) {
-                const u32x4_t v = st.x[i][t];
-                if constexpr (WF == WF_Q4_0) {
-                    // lo: elements 4 g .. 4 g + 3, hi: 16 + 4 g ..; nibble pairs (0, 2), (1, 3)
-                    st.x[i][t] = u32x4_t{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[1], v[0], 0x07060302u),
-                                         __builtin_amdgcn_perm(v[3], v[2], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
-                } else if constexpr (WF == WF_AFFINE4) {
-                    // byte i holds elements 2 i and 2 i + 1: pairs (0, 4), (2, 6), (1, 5), (3, 7)
-                    st.x[i][t] = u32x4_t{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x05040100u),
-                                         __builtin_amdgcn_perm(v[2], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-                }
-            }
+            for (int t = 0; t < 4; t++)
+                x[i][t] = *reinterpret_cast<const u32x4_t*>(xs + (local * 4 + t) * x_rows * 64 + xat[i]);
         if constexpr (WF == WF_Q4_0) {
 #pragma unroll
-            for (int n = 0; n < NT; n++) transpose4(st.w[n].q[0]);
+            for (int n = 0; n < NT; n++) transpose4(w[n].q[0]);
 #pragma unroll
             for (int t = 0; t < 4; t++) {
                 floatx4_t c0[MT];
 #pragma unroll
                 for (int i = 0; i < MT; i++)
-                    c0[i] = XDT == DT_BF16 ? mfma16<XDT>(st.x[i][t], splat(0xC308C308u), zero) : zero;      // -136 sum x
+                    c0[i] = XDT == DT_BF16 ? mfma16<XDT>(x[i][t], splat(0xC308C308u), zero) : zero;      // -136 sum x
 #pragma unroll
                 for (int n = 0; n < NT; n++) {
-                    const u32x4_t w = nibbles<XDT, 8>(st.w[n].q[0][t], mask);
-                    const float d = f16_to_f32((st.w[n].s[t >> 1] >> (16 * (t & 1))) & 0xFFFFu);
+                    const u32x4_t c = nibbles<XDT, 8>(w[n].q[0][t], mask);
+                    const float d = scale(w[n], t);
 #pragma unroll
                     for (int i = 0; i < MT; i++) {
-                        const floatx4_t v = mfma16<XDT>(st.x[i][t], w, c0[i]);
+                        const floatx4_t v = mfma16<XDT>(x[i][t], c, c0[i]);
 #pragma unroll
                         for (int e = 0; e < 4; e++) acc[i][n][e] = fmaf(d, v[e], acc[i][n][e]);
                     }
@@ -271,7 +329,7 @@ __global__ __launch_bounds__(NT * MT <= 3 ? 1024 : 512) void k_linear_few(const 
         } else {
             if constexpr (WF == WF_AFFINE4) {
 #pragma unroll
-                for (int n = 0; n < NT; n++) transpose4(st.w[n].q[0]);
+                for (int n = 0; n < NT; n++) transpose4(w[n].q[0]);
             }
             // 4 bits, bfloat16: the codes are 128 + q, so the sums of x enter as -128 sum x
             constexpr bool kOffset = WF == WF_AFFINE4 && XDT == DT_BF16;
@@ -281,23 +339,22 @@ __global__ __launch_bounds__(NT * MT <= 3 ? 1024 : 512) void k_linear_few(const 
                 floatx4_t cs[MT];
 #pragma unroll
                 for (int i = 0; i < MT; i++)
-                    cs[i] = mfma16<XDT>(st.x[i][2 * h + 1], splat(one), mfma16<XDT>(st.x[i][2 * h], splat(one), zero));
+                    cs[i] = mfma16<XDT>(x[i][2 * h + 1], splat(one), mfma16<XDT>(x[i][2 * h], splat(one), zero));
 #pragma unroll
                 for (int n = 0; n < NT; n++) {
                     u32x4_t w0, w1;
                     if constexpr (WF == WF_AFFINE4) {
-                        w0 = nibbles<XDT, 0>(st.w[n].q[0][2 * h], mask);
-                        w1 = nibbles<XDT, 0>(st.w[n].q[0][2 * h + 1], mask);
+                        w0 = nibbles<XDT, 0>(w[n].q[0][2 * h], mask);
+                        w1 = nibbles<XDT, 0>(w[n].q[0][2 * h + 1], mask);
                     } else {
-                        w0 = bytes8<XDT>(st.w[n].q[h][0], st.w[n].q[h][1]);
-                        w1 = bytes8<XDT>(st.w[n].q[h][2], st.w[n].q[h][3]);
+                        w0 = bytes8<XDT>(w[n].q[h][0], w[n].q[h][1]);
+                        w1 = bytes8<XDT>(w[n].q[h][2], w[n].q[h][3]);
                     }
-                    const float s = bf16_to_f32((st.w[n].s[0] >> (16 * h)) & 0xFFFFu);
-                    const float b = bf16_to_f32((st.w[n].s[1] >> (16 * h)) & 0xFFFFu) * (kOffset ? -0.0078125f : 1.0f);
+                    const float s = scale(w[n], h), b = bias(w[n], h) * (kOffset ? -0.0078125f : 1.0f);
 #pragma unroll
                     for (int i = 0; i < MT; i++) {
                         const floatx4_t v =
-                            mfma16<XDT>(st.x[i][2 * h + 1], w1, mfma16<XDT>(st.x[i][2 * h], w0, kOffset ? cs[i] : zero));
+                            mfma16<XDT>(x[i][2 * h + 1], w1, mfma16<XDT>(x[i][2 * h], w0, kOffset ? cs[i] : zero));
 #pragma unroll
                         for (int e = 0; e < 4; e++) acc[i][n][e] = fmaf(b, cs[i][e], fmaf(s, v[e], acc[i][n][e]));
                     }
@@ -306,33 +363,153 @@ __global__ __launch_bounds__(NT * MT <= 3 ? 1024 : 512) void k_linear_few(const 
         }
     };
 
-    // chunks wave, wave + waves, ..: the next one loads while this one multiplies
-    if (wave < chunks) {
-        Stage s0, s1;
-        load(wave, s0);
-        for (int c = wave;;) {
-            const int c1 = c + waves;
-            load(c1 < chunks ? c1 : c, s1);
+    // A wave takes steps wave, wave + waves, ..
+    constexpr int kChunks = kStep / 128;                     // of a step
+    uint8_t* codes = lds + wave * NT * kStepB;
+    uint8_t* scales = lds + kRing + wave * NT * kScaleB;
+    // The step in flight (nothing later is) into registers: its scales change
+    // places in LDS, its copies have landed.
+    auto take = [&](Codes (&w)[kChunks][NT]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < kSL; e++)
+            if (e * 4 + g < NT) *reinterpret_cast<u32x4_t*>(scales + (e * 64 + lane) * 16) = sc[e];
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        Q4_WAIT_VMCNT(0);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            u32x4_t q[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                q[h] = *reinterpret_cast<const u32x4_t*>(codes + n * kStepB + j * 128 + (((4 * h + g) ^ (j & 7)) * 16));
+            const u32x4_t s = *reinterpret_cast<const u32x4_t*>(scales + (n * 16 + j) * 16);
+            if constexpr (WF == WF_AFFINE8) {
+                w[0][n] = Codes{{q[0], q[1]}, {s[0], s[2]}};
+            } else {
+#pragma unroll
+                for (int h = 0; h < kChunks; h++)
+                    w[h][n] = WF == WF_Q4_0 ? Codes{{q[h]}, {s[2 * h], s[2 * h + 1]}} : Codes{{q[h]}, {s[h], s[2 + h]}};
+            }
+        }
+        // the reads are in registers before the next copies overwrite them
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_s_waitcnt(0xC07F);                  // lgkmcnt(0)
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    };
+    if constexpr (DIAG) {
+        // x is staged for `round` steps of every wave at a time, all of K as a
+        // rule.  Its first pieces are requested before the codes (loads return in
+        // order), so that x waits in LDS when the codes arrive.
+        const int round = kX / (x_rows * 256 * kChunks) / waves;
+        const int most = round * waves * kChunks, all = steps * kChunks;
+        const int piece_shift = 4 + x_shift;                 // pieces of a chunk: 16 x_rows
+        constexpr int kEarly = 4;
+        u32x4_t early[kEarly];
+        const int pieces0 = (all < most ? all : most) << piece_shift;
+#pragma unroll
+        for (int e = 0; e < kEarly; e++) {
+            const int u = (int)(threadIdx.x + e * blockDim.x);
+            early[e] = x_piece(u >> piece_shift, u);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        request(wave);                                       // waves <= steps
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = 0; e < kEarly; e++) {
+            const int u = (int)(threadIdx.x + e * blockDim.x);
+            if (u < pieces0) x_put(u, early[e]);
+        }
+        for (int r0 = 0; r0 * waves < steps; r0 += round) {
+            if (r0 > 0) __syncthreads();
+            const int first = r0 * waves * kChunks, left = all - first;
+            const int pieces = (left < most ? left : most) << piece_shift;
+            for (int u = (r0 == 0 ? kEarly * (int)blockDim.x : 0) + (int)threadIdx.x; u < pieces; u += blockDim.x)
+                x_put(u, x_piece(first + (u >> piece_shift), u));
+            __syncthreads();
+            for (int r = r0; r < r0 + round; r++) {
+                const int step = r * waves + wave;
+                if (step >= steps) break;
+                Codes w[kChunks][NT];
+                take(w);
+                if (step + waves < steps) request(step + waves);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int h = 0; h < kChunks; h++) compute(w[h], step * kChunks + h - first);
+            }
+        }
+    } else {
+        // x of kXC chunks of every wave at a time, requested into registers before
+        // the codes of the step after, so that it does not wait behind them
+        constexpr int kXC = MT == 1 ? kChunks : 1, kXP = kXC * MT * 4;       // pieces a thread
+        static_assert(kMaxWaves * kXC * MT * 16 * 256 <= kX, "x of a round fits");
+        u32x4_t xn[kXP];
+        const int piece_shift = 4 + x_shift, pieces = (waves * kXC) << piece_shift;
+        auto x_request = [&](int r, int h) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < kXP; e++) {
+                const int u = (int)(threadIdx.x + e * blockDim.x), lc = u >> piece_shift;
+                xn[e] = x_piece((r * waves + lc / kXC) * kChunks + h + lc % kXC, u);
+            }
             __builtin_amdgcn_sched_barrier(0);
-            compute(s0);
-            if (c1 >= chunks) break;
-            const int c2 = c1 + waves;
-            load(c2 < chunks ? c2 : c1, s0);
-            __builtin_amdgcn_sched_barrier(0);
-            compute(s1);
-            if (c2 >= chunks) break;
-            c = c2;
+        };
+        auto x_swap = [&]() __attribute__((always_inline)) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kXP; e++) {
+                const int u = (int)(threadIdx.x + e * blockDim.x);
+                if (u < pieces) x_put(u, xn[e]);
+            }
+            __syncthreads();
+        };
+        x_request(0, 0);
+        request(wave);
+        for (int r = 0; r * waves < steps; r++) {
+            const int step = r * waves + wave;
+            Codes w[kChunks][NT];
+            x_swap();
+            const bool live = step < steps;
+            if (live) take(w);
+            if (kXC == kChunks) {
+                x_request(r + 1, 0);
+                if (step + waves < steps) request(step + waves);
+                __builtin_amdgcn_sched_barrier(0);
+                if (live) {
+#pragma unroll
+                    for (int h = 0; h < kChunks; h++) compute(w[h], wave * kXC + h);
+                }
+            } else {
+                x_request(r, 1);
+                if (step + waves < steps) request(step + waves);
+                __builtin_amdgcn_sched_barrier(0);
+                if (live) compute(w[0], wave);
+                x_swap();
+                x_request(r + 1, 0);
+                if (live) compute(w[kChunks - 1], wave);
+            }
         }
     }
+    __syncthreads();
 
-    // lane: column j, rows 4 g + e of each 16 x 16 tile
+    // lane: column j, rows 4 g + e of each 16 x 16 tile (DIAG: row g, its blocks)
 #pragma unroll
-    for (int n = 0; n < NT; n++)
+    for (int n = 0; n < NT; n++) {
+        if constexpr (kBlocks) {
+            red[(wave * NT + n) * kTile + g * 16 + j] = (acc[0][n][0] + acc[0][n][1]) + (acc[0][n][2] + acc[0][n][3]);
+            continue;
+        }
+        if constexpr (DIAG) {
+            if (g == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) red[(wave * NT + n) * kTile + e * 16 + j] = acc[0][n][e];
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < MT; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 red[(wave * NT + n) * kTile + (i * 16 + 4 * g + e) * 16 + j] = acc[i][n][e];
+    }
     __syncthreads();
     for (int o = threadIdx.x; o < M * kCols * 16; o += blockDim.x) {
         const int col = o & 15, p = (o >> 4) % kCols, m = (o >> 4) / kCols;
@@ -361,34 +538,33 @@ __global__ __launch_bounds__(NT * MT <= 3 ? 1024 : 512) void k_linear_few(const 
 
 // ---- host ------------------------------------------------------------------------
 
-template <int WF, int XDT, int MT, int P, bool GATED>
+template <int WF, int XDT, int MT, int P, bool GATED, bool DIAG>
 void few_launch(const LinearArgs& a, hipStream_t s) {
-    constexpr int NT = GATED ? 2 * P : P;
-    constexpr int kMaxWaves = NT * MT <= 3 ? 16 : 8;
-    const int64_t chunks = (a.K + 127) / 128;
-    const int waves = (int)(chunks < kMaxWaves ? chunks : kMaxWaves);
+    constexpr int kStep = WF == WF_AFFINE8 ? 128 : 256;
+    const int64_t steps = (a.K + kStep - 1) / kStep, most = few_waves<MT, DIAG>();
+    int x_shift = 0;
+    while ((1 << x_shift) < a.M) x_shift++;
     const unsigned grid = (unsigned)((a.N + 16 * P - 1) / (16 * P));
-    hipLaunchKernelGGL((k_linear_few<WF, XDT, MT, NT, GATED>), dim3(grid), dim3(64 * waves), 0, s, a);
+    hipLaunchKernelGGL((k_linear_few<WF, XDT, MT, GATED ? 2 * P : P, GATED, DIAG>), dim3(grid),
+                       dim3(64 * (unsigned)(steps < most ? steps : most)), 0, s, a, x_shift);
 }
-template <int WF, int XDT, int MT, bool GATED>
+template <int WF, int XDT, int MT, bool DIAG>
 void few_tiles(const LinearArgs& a, hipStream_t s) {
-    // as few column tiles a workgroup as fill the CUs: each workgroup reads all of x
+    // Column tiles of a workgroup: as few as fill the CUs, since every workgroup
+    // reads all of x; one pair at q4_gated (12288 x 4096: 17.6 us at one row
+    // against 18.1 with three pairs, 41.0 at 32 rows against 42.7 with two),
+    // at most two tiles above four rows (registers)
     const int64_t tiles = (a.N + 15) / 16, cus = current_cu_count();
-    if (tiles <= cus) few_launch<WF, XDT, MT, 1, GATED>(a, s);
-    else if (tiles <= 2 * cus || (MT == 4 && GATED)) few_launch<WF, XDT, MT, 2, GATED>(a, s);
-    else few_launch<WF, XDT, MT, (MT == 4 && GATED) ? 2 : 3, GATED>(a, s);
+    if (a.nmat == 2) few_launch<WF, XDT, MT, 1, true, DIAG>(a, s);
+    else if (tiles <= cus) few_launch<WF, XDT, MT, 1, false, DIAG>(a, s);
+    else if (tiles <= 2 * cus || !DIAG) few_launch<WF, XDT, MT, 2, false, DIAG>(a, s);
+    else few_launch<WF, XDT, MT, DIAG ? 3 : 2, false, DIAG>(a, s);
 }
 template <int WF, int XDT>
 void few_rows(const LinearArgs& a, hipStream_t s) {
-    if (a.nmat == 2) {
-        if (a.M <= 16) few_tiles<WF, XDT, 1, true>(a, s);
-        else if (a.M <= 32) few_tiles<WF, XDT, 2, true>(a, s);
-        else few_tiles<WF, XDT, 4, true>(a, s);
-    } else {
-        if (a.M <= 16) few_tiles<WF, XDT, 1, false>(a, s);
-        else if (a.M <= 32) few_tiles<WF, XDT, 2, false>(a, s);
-        else few_tiles<WF, XDT, 4, false>(a, s);
-    }
+    if (a.M <= 4) few_tiles<WF, XDT, 1, true>(a, s);
+    else if (a.M <= 16) few_tiles<WF, XDT, 1, false>(a, s);
+    else few_tiles<WF, XDT, 2, false>(a, s);
 }
 template <int WF>
 hipError_t few_format(const LinearArgs& a, hipStream_t s) {

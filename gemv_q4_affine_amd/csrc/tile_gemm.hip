@@ -36,15 +36,6 @@ namespace q4 {
 
 constexpr int kRing = 4;
 
-// One direct-to-LDS copy of a unit: lane l's 16 bytes at src + 16 l land at LDS
-// address m0 + 16 l.  Inline assembly, so that the compiler does not take it
-// for an LDS store and wait for every copy in flight before each read; the
-// ring's own waits order the copies with the reads.  No register receives data.
-__device__ __forceinline__ void copy_unit(const uint8_t* src, uint32_t voff, uint32_t m0) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(src), "s"(m0)
-                 : "memory", "m0");
-}
-
 template <int NT, int MT, int EPI>
 __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     static_assert(EPI != EPI_GATED || NT % 2 == 0, "gate and up panels come in pairs");
