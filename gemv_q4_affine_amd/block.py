@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from .binding import (Q4_FMT_AFFINE4, Q4_FMT_AFFINE8, Q4_FMT_Q4_0, _alloc_stream, _check, _dt, _empty, _p, _stream, lib as _base_lib)
+from .binding import Q4_FMT_AFFINE4, Q4_FMT_AFFINE8, Q4_FMT_Q4_0, _DT, _alloc_stream, _check, _dt, _stream, lib as _base_lib
 
 Q4_ACT_NONE, Q4_ACT_SILU, Q4_ACT_GELU, Q4_ACT_GELU_TANH, Q4_ACT_RELU = 0, 1, 2, 3, 4
 Q4_NORM_NONE, Q4_NORM_RMS, Q4_NORM_LAYER = 0, 1, 2
@@ -53,25 +53,68 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _planes(w, fmt=None):
+# The marshalling is on the clock of a call on one token (its kernels take 3 to
+# 20 us), so it is kept short: pointers as plain ints, the stream's handle
+# without a Stream object, outputs like their inputs where the shape is theirs.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, like):
+    """The hipStream_t of a call: the caller's stream, or the current one of the tensor's GPU."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(like.get_device())
+    return _stream(stream)
+
+
+def _ptr(t):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        return t                       # raw pointer (int) passed through
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _new(shape, dtype, like, stream):
+    """An output, owned by the call's stream."""
+    if stream is None:
+        if shape == like.shape and dtype == like.dtype:
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(_alloc_stream(stream)):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _planes(w):
     """(format, N, K, three plane pointers) of a weight tuple."""
-    if len(w) not in (2, 3):
+    n = len(w)
+    if n not in (2, 3):
         raise ValueError("a weight is (qs, d) or (codes, scales, biases)")
     q, s = w[0], w[1]
-    if fmt is None:
-        fmt = Q4_FMT_Q4_0 if len(w) == 2 else Q4_FMT_AFFINE8 if q.shape[-1] == s.shape[1] * 64 else Q4_FMT_AFFINE4
-    N, K = s.shape[0], s.shape[1] * (32 if fmt == Q4_FMT_Q4_0 else 64)
-    want = {Q4_FMT_Q4_0: N * K // 2, Q4_FMT_AFFINE4: N * K // 2, Q4_FMT_AFFINE8: N * K}[fmt]
-    if q.numel() * q.element_size() != want or any(t.shape != s.shape for t in w[2:]):
+    N, groups = s.shape
+    if n == 2:
+        fmt, K, want = Q4_FMT_Q4_0, groups * 32, groups * 16
+    elif q.shape[-1] == groups * 64:
+        fmt, K, want = Q4_FMT_AFFINE8, groups * 64, groups * 64
+    else:
+        fmt, K, want = Q4_FMT_AFFINE4, groups * 64, groups * 32
+    if q.numel() != N * want or q.element_size() != 1 or s.element_size() != 2 or (n == 3 and w[2].shape != s.shape):
         raise ValueError("the planes of a weight do not fit each other")
-    return fmt, N, K, (_p(q), _p(s), _p(w[2]) if len(w) == 3 else None)
+    return fmt, N, K, (_ptr(q), _ptr(s), _ptr(w[2]) if n == 3 else None)
 
 
 def _like(t, name, shape, dtype):
     """An optional tensor of the given shape and dtype (raw pointers pass through)."""
-    if isinstance(t, torch.Tensor) and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and isinstance(t, torch.Tensor) and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     return t
+
+
+def _out(t, name, shape, dtype, like, stream):
+    return _new(shape, dtype, like, stream) if t is None else _like(t, name, shape, dtype)
 
 
 def _workspace(workspace, n, like, stream):
@@ -79,14 +122,14 @@ def _workspace(workspace, n, like, stream):
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
-        workspace = _empty((n,), torch.uint8, like, stream) if n > 0 else None
+        return (_new((n,), torch.uint8, like, stream), n) if n > 0 else (None, 0)
     return workspace, workspace.numel() * workspace.element_size() if workspace is not None else 0
 
 
 def _summed(t, name, shape, dtype, terms, like, stream):
     """An output that sums over `terms` rows or columns: allocated if None,
     and zero where there are none (the library writes nothing then)."""
-    t = _empty(shape, dtype, like, stream) if t is None else _like(t, name, shape, dtype)
+    t = _out(t, name, shape, dtype, like, stream)
     if terms == 0 and t.numel():
         with torch.cuda.stream(_alloc_stream(stream)):
             t.zero_()
@@ -108,13 +151,13 @@ def q4_linear(w, x, bias=None, act=Q4_ACT_NONE, residual=None, save_pre=False, y
     _like(x, "x", (M, K), x.dtype)
     _like(bias, "bias", (N,), x.dtype)
     _like(residual, "residual", (M, N), x.dtype)
-    y = _empty((M, N), x.dtype, x, stream) if y is None else _like(y, "y", (M, N), x.dtype)
+    y = _out(y, "y", (M, N), x.dtype, x, stream)
     if pre is None and save_pre:
-        pre = _empty((M, N), x.dtype, x, stream)
+        pre = _new((M, N), x.dtype, x, stream)
     _like(pre, "pre", (M, N), x.dtype)
     ws, n = _workspace(workspace, q4_linear_workspace_size(M, N, K, fmt), x, stream)
-    _check("q4_linear", lib().q4_linear(fmt, *wp, _p(bias), act, _p(residual), _p(x), _dt(x), _p(y), _p(pre), M, N, K,
-                                        _p(ws), n, _stream(stream)))
+    _check("q4_linear", lib().q4_linear(fmt, *wp, _ptr(bias), act, _ptr(residual), _ptr(x), _dt(x), _ptr(y), _ptr(pre), M, N, K,
+                                        _ptr(ws), n, _handle(stream, x)))
     return y if pre is None else (y, pre)
 
 
@@ -132,13 +175,13 @@ def q4_linear_backward(w, dy, act=Q4_ACT_NONE, pre=None, bias_grad=False, dx=Non
     _like(pre, "pre", (M, N), dy.dtype)
     out = {"dx": _summed(dx, "dx", (M, K), dy.dtype, N, dy, stream)}
     if act != Q4_ACT_NONE:
-        out["dz"] = _empty((M, N), dy.dtype, dy, stream) if dz is None else _like(dz, "dz", (M, N), dy.dtype)
+        out["dz"] = _out(dz, "dz", (M, N), dy.dtype, dy, stream)
     if bias_grad or dbias is not None:
         out["dbias"] = _summed(dbias, "dbias", (N,), torch.float32, M, dy, stream)
     ws, n = _workspace(workspace, q4_linear_backward_workspace_size(M, N, K, fmt), dy, stream)
     _check("q4_linear_backward",
-           lib().q4_linear_backward(fmt, *wp, act, _p(pre), _p(dy), _dt(dy), _p(out["dx"]), _p(out.get("dz")),
-                                    _p(out.get("dbias")), M, N, K, _p(ws), n, _stream(stream)))
+           lib().q4_linear_backward(fmt, *wp, act, _ptr(pre), _ptr(dy), _dt(dy), _ptr(out["dx"]), _ptr(out.get("dz")),
+                                    _ptr(out.get("dbias")), M, N, K, _ptr(ws), n, _handle(stream, dy)))
     return out
 
 
@@ -165,15 +208,15 @@ def q4_gated(gate, up, x, act=Q4_ACT_SILU, gate_bias=None, up_bias=None, save_pr
     _like(x, "x", (M, K), x.dtype)
     _like(gate_bias, "gate_bias", (N,), x.dtype)
     _like(up_bias, "up_bias", (N,), x.dtype)
-    h = _empty((M, N), x.dtype, x, stream) if h is None else _like(h, "h", (M, N), x.dtype)
+    h = _out(h, "h", (M, N), x.dtype, x, stream)
     if save_pre:
-        gate_pre = _empty((M, N), x.dtype, x, stream) if gate_pre is None else gate_pre
-        up_pre = _empty((M, N), x.dtype, x, stream) if up_pre is None else up_pre
+        gate_pre = _new((M, N), x.dtype, x, stream) if gate_pre is None else gate_pre
+        up_pre = _new((M, N), x.dtype, x, stream) if up_pre is None else up_pre
     _like(gate_pre, "gate_pre", (M, N), x.dtype)
     _like(up_pre, "up_pre", (M, N), x.dtype)
     ws, n = _workspace(workspace, q4_gated_workspace_size(M, N, K, fmt), x, stream)
-    _check("q4_gated", lib().q4_gated(fmt, *gp, *upp, _p(gate_bias), _p(up_bias), act, _p(x), _dt(x), _p(h),
-                                      _p(gate_pre), _p(up_pre), M, N, K, _p(ws), n, _stream(stream)))
+    _check("q4_gated", lib().q4_gated(fmt, *gp, *upp, _ptr(gate_bias), _ptr(up_bias), act, _ptr(x), _dt(x), _ptr(h),
+                                      _ptr(gate_pre), _ptr(up_pre), M, N, K, _ptr(ws), n, _handle(stream, x)))
     return h if gate_pre is None else (h, gate_pre, up_pre)
 
 
@@ -189,16 +232,16 @@ def q4_gated_backward(gate, up, dh, gate_pre, up_pre, act=Q4_ACT_SILU, bias_grad
     for t, name in ((dh, "dh"), (gate_pre, "gate_pre"), (up_pre, "up_pre"), (dgate, "dgate"), (dup, "dup")):
         _like(t, name, (M, N), dh.dtype)
     out = {"dx": _summed(dx, "dx", (M, K), dh.dtype, N, dh, stream),
-           "dgate": _empty((M, N), dh.dtype, dh, stream) if dgate is None else dgate,
-           "dup": _empty((M, N), dh.dtype, dh, stream) if dup is None else dup}
+           "dgate": _new((M, N), dh.dtype, dh, stream) if dgate is None else dgate,
+           "dup": _new((M, N), dh.dtype, dh, stream) if dup is None else dup}
     for name, t in (("dgate_bias", dgate_bias), ("dup_bias", dup_bias)):
         if bias_grad or t is not None:
             out[name] = _summed(t, name, (N,), torch.float32, M, dh, stream)
     ws, n = _workspace(workspace, q4_gated_backward_workspace_size(M, N, K, fmt), dh, stream)
     _check("q4_gated_backward",
-           lib().q4_gated_backward(fmt, *gp, *upp, act, _p(gate_pre), _p(up_pre), _p(dh), _dt(dh), _p(out["dx"]),
-                                   _p(out["dgate"]), _p(out["dup"]), _p(out.get("dgate_bias")), _p(out.get("dup_bias")),
-                                   M, N, K, _p(ws), n, _stream(stream)))
+           lib().q4_gated_backward(fmt, *gp, *upp, act, _ptr(gate_pre), _ptr(up_pre), _ptr(dh), _dt(dh), _ptr(out["dx"]),
+                                   _ptr(out["dgate"]), _ptr(out["dup"]), _ptr(out.get("dgate_bias")), _ptr(out.get("dup_bias")),
+                                   M, N, K, _ptr(ws), n, _handle(stream, dh)))
     return out
 
 
@@ -221,6 +264,12 @@ def _gate_rows(gate, gate_rows, M):
     return gate_rows
 
 
+def _code(dtype):
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return _DT[dtype]
+
+
 def _vectors(D, dtype, **named):
     for name, t in named.items():
         _like(t, name, (D,), dtype)
@@ -238,25 +287,21 @@ def block_norm(r, y=None, pre_norm=Q4_NORM_RMS, pre_weight=None, pre_bias=None, 
     dt = y.dtype if y is not None else (dtype or r.dtype)
     if y is not None:
         _like(y, "y", (M, D), dt)
-        r_out = _empty((M, D), r.dtype, r, stream) if r_out is None else _like(r_out, "r_out", (M, D), r.dtype)
+        r_out = _out(r_out, "r_out", (M, D), r.dtype, r, stream)
     _vectors(D, dt, pre_weight=pre_weight, pre_bias=pre_bias, post_weight=post_weight, post_bias=post_bias)
     rows = _gate_rows(gate, gate_rows, M)
     if gate is not None:
         _like(gate, "gate", (gate.shape[0], D), dt)
     if pre_norm != Q4_NORM_NONE:
-        n = _empty((M, D), dt, r, stream) if n is None else _like(n, "n", (M, D), dt)
+        n = _out(n, "n", (M, D), dt, r, stream)
     if stats is None and save_stats:
-        stats = _empty((M, 4), torch.float32, r, stream)
+        stats = _new((M, 4), torch.float32, r, stream)
     _like(stats, "stats", (M, 4), torch.float32)
     _check("block_norm",
-           lib().block_norm(_p(y), _p(r), _code(dt), _dt(r), M, D, post_norm, _p(post_weight), _p(post_bias), _p(gate),
-                            rows, scale, pre_norm, _p(pre_weight), _p(pre_bias), eps, _p(r_out), _p(n), _p(stats),
-                            _stream(stream)))
+           lib().block_norm(_ptr(y), _ptr(r), _code(dt), _dt(r), M, D, post_norm, _ptr(post_weight), _ptr(post_bias), _ptr(gate),
+                            rows, scale, pre_norm, _ptr(pre_weight), _ptr(pre_bias), eps, _ptr(r_out), _ptr(n), _ptr(stats),
+                            _handle(stream, r)))
     return r if y is None else r_out, n, stats
-
-
-def _code(dtype):
-    return _dt(torch.empty(0, dtype=dtype))
 
 
 def block_norm_backward_workspace_size(M, D, gate_rows=1) -> int:
@@ -277,19 +322,19 @@ def block_norm_backward(r_out, y, stats, dn=None, dr_out=None, pre_norm=Q4_NORM_
     _like(stats, "stats", (M, 4), torch.float32)
     _vectors(D, dt, pre_weight=pre_weight, pre_bias=pre_bias, post_weight=post_weight, post_bias=post_bias)
     rows = _gate_rows(gate, gate_rows, M)
-    out = {"dr": _empty((M, D), r_out.dtype, r_out, stream)}
+    out = {"dr": _new((M, D), r_out.dtype, r_out, stream)}
     if y is not None:
-        out["dy"] = _empty((M, D), dt, r_out, stream)
+        out["dy"] = _new((M, D), dt, r_out, stream)
     if gate is not None:
-        out["dgate"] = _empty(_like(gate, "gate", (gate.shape[0], D), dt).shape, dt, r_out, stream)
+        out["dgate"] = _new(_like(gate, "gate", (gate.shape[0], D), dt).shape, dt, r_out, stream)
     for name, t in (("pre_dw", pre_weight), ("pre_db", pre_bias), ("post_dw", post_weight), ("post_db", post_bias)):
         if t is not None:
             out[name] = _summed(None, name, (D,), torch.float32, M, r_out, stream)
     ws, n = _workspace(workspace, block_norm_backward_workspace_size(M, D, rows), r_out, stream)
     _check("block_norm_backward",
-           lib().block_norm_backward(_p(y), _p(r_out), _p(stats), _p(dn), _p(dr_out), _code(dt), _dt(r_out), M, D,
-                                     post_norm, _p(post_weight), _p(post_bias), _p(gate), rows, scale, pre_norm,
-                                     _p(pre_weight), _p(out["dr"]), _p(out.get("dy")), _p(out.get("dgate")),
-                                     _p(out.get("pre_dw")), _p(out.get("pre_db")), _p(out.get("post_dw")),
-                                     _p(out.get("post_db")), _p(ws), n, _stream(stream)))
+           lib().block_norm_backward(_ptr(y), _ptr(r_out), _ptr(stats), _ptr(dn), _ptr(dr_out), _code(dt), _dt(r_out), M, D,
+                                     post_norm, _ptr(post_weight), _ptr(post_bias), _ptr(gate), rows, scale, pre_norm,
+                                     _ptr(pre_weight), _ptr(out["dr"]), _ptr(out.get("dy")), _ptr(out.get("dgate")),
+                                     _ptr(out.get("pre_dw")), _ptr(out.get("pre_db")), _ptr(out.get("post_dw")),
+                                     _ptr(out.get("post_db")), _ptr(ws), n, _handle(stream, r_out)))
     return out
