@@ -32,57 +32,74 @@ __device__ __forceinline__ RowScale<WF> row_scale(const QuantW& w, int64_t n, in
     }
 }
 
-// Image of W: lane (row j, half h) of a wave takes whole blocks of 32 weights,
-// block 2 t + h of the row in pass t, and writes each as its four 16-byte
-// pieces; for one piece 32 lanes write 512 contiguous bytes.  A wave does 256
-// weights of a row (a row's 128 contiguous code bytes at 4 bits), four waves a
-// workgroup.
+// Image of W: a wave takes a panel's 32 rows by 128 bytes of codes (256 weights;
+// 128 at 8 bits).  Direct-to-LDS copies of 8 rows by 128 contiguous bytes (a load
+// whose neighbouring lanes lie on different rows asks for 64 separate pieces),
+// the pieces of 16 bytes placed by an XOR with the row; then lane (row j, half h)
+// takes whole blocks of 32 weights, block 2 t + h in pass t, and writes each as
+// its four 16-byte pieces: for one piece 32 lanes write 512 contiguous bytes.
 template <int WF>
 __global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int mats, int N, int64_t K, int64_t slices,
                                                       int64_t kgroups, uint8_t* __restrict__ img) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 31, h = lane >> 5;
+    constexpr int kBlocks = WF == WF_AFFINE8 ? 4 : 8;        // of 32 weights, in a wave's 128 bytes of a row
+    constexpr int kPieces = 8 / kBlocks;                     // 16-byte pieces of a block
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * 32 * 128];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), j = lane & 31, h = lane >> 5;
     const int64_t panel = blockIdx.x / kgroups;
     const QuantW w = mats == 2 && (panel & 1) ? w1 : w0;
-    int64_t n = panel / mats * 32 + j;
-    n = n < N ? n : N - 1;                   // rows past N: their outputs are never stored
-    const int64_t nb = K / 32, b0 = (blockIdx.x % kgroups * 4 + wave) * 8;
-    constexpr int kWords = WF == WF_AFFINE8 ? 2 : 1;
-    u32x4_t raw[4][kWords];
-    RowScale<WF> sc[4];
+    const int64_t first = panel / mats * 32, in = N - 1 - first;
+    const int64_t nb = K / 32, b0 = (blockIdx.x % kgroups * 4 + wave) * kBlocks;
+    if (b0 >= nb) return;                                    // no barrier below: a wave's LDS is its own
+    const uint32_t row_q = (uint32_t)(WF == WF_AFFINE8 ? K : K / 2), last = row_q / 16 - 1;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds) +
+                          (uint32_t)wave * 4096;
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
+    for (int c = 0; c < 4; c++) {
+        // rows past N repeat the last one (their outputs are never stored), pieces
+        // past the row its last (never written)
+        const uint32_t r = (uint32_t)(8 * c + (lane >> 3)), row = r < (uint32_t)in ? r : (uint32_t)in;
+        const uint32_t p = (uint32_t)b0 * kPieces + ((uint32_t)(lane & 7) ^ (r & 7u));
+        copy_unit(w.q + first * row_q, row * row_q + (p < last ? p : last) * 16u, lds0 + c * 1024);
+    }
+    const int64_t n = first + (j < in ? j : in);
+    RowScale<WF> sc[kBlocks / 2];
+#pragma unroll
+    for (int t = 0; t < kBlocks / 2; t++) {
         int64_t b = b0 + 2 * t + h;
         b = b < nb ? b : nb - 1;
-        const u32x4_t* q = reinterpret_cast<const u32x4_t*>(w.q + (n * nb + b) * (16 * kWords));
-#pragma unroll
-        for (int e = 0; e < kWords; e++) raw[t][e] = __builtin_nontemporal_load(q + e);
         sc[t] = row_scale<WF>(w, n, b, K);
     }
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    Q4_WAIT_VMCNT(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
+    for (int t = 0; t < kBlocks / 2; t++) {
         const int64_t b = b0 + 2 * t + h;
         if (b >= nb) continue;
+        u32x4_t raw[kPieces];
+#pragma unroll
+        for (int e = 0; e < kPieces; e++)
+            raw[e] = *reinterpret_cast<const u32x4_t*>(lds + wave * 4096 + j * 128 + ((((2 * t + h) * kPieces + e) ^ (j & 7)) * 16));
         uint8_t* out = img + (panel * slices + 2 * b) * kUnit + j * 16;
 #pragma unroll
         for (int c = 0; c < 4; c++) {        // elements 8 c .. 8 c + 7: slice c / 2, half c % 2
             float f[8];
+            uint32_t lo, hi;
             if constexpr (WF == WF_AFFINE8) {
-                const uint32_t lo = raw[t][c >> 1][2 * (c & 1)], hi = raw[t][c >> 1][2 * (c & 1) + 1];
-                f[0] = byte_f32<0>(lo); f[1] = byte_f32<1>(lo); f[2] = byte_f32<2>(lo); f[3] = byte_f32<3>(lo);
-                f[4] = byte_f32<0>(hi); f[5] = byte_f32<1>(hi); f[6] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
+                lo = raw[c >> 1][2 * (c & 1)];
+                hi = raw[c >> 1][2 * (c & 1) + 1];
             } else if constexpr (WF == WF_Q4_0) {
                 // elements 0..15 low nibbles, 16..31 high nibbles of bytes 0..15
-                const uint32_t m = 0x0F0F0F0Fu;
-                const uint32_t lo = (c < 2 ? raw[t][0][2 * (c & 1)] : raw[t][0][2 * (c & 1)] >> 4) & m;
-                const uint32_t hi = (c < 2 ? raw[t][0][2 * (c & 1) + 1] : raw[t][0][2 * (c & 1) + 1] >> 4) & m;
-                f[0] = byte_f32<0>(lo); f[1] = byte_f32<1>(lo); f[2] = byte_f32<2>(lo); f[3] = byte_f32<3>(lo);
-                f[4] = byte_f32<0>(hi); f[5] = byte_f32<1>(hi); f[6] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
+                lo = (raw[0][2 * (c & 1)] >> (c < 2 ? 0 : 4)) & 0x0F0F0F0Fu;
+                hi = (raw[0][2 * (c & 1) + 1] >> (c < 2 ? 0 : 4)) & 0x0F0F0F0Fu;
             } else {
                 // byte i: elements 2 i (low nibble) and 2 i + 1
-                const uint32_t lo = raw[t][0][c] & 0x0F0F0F0Fu, hi = (raw[t][0][c] >> 4) & 0x0F0F0F0Fu;
-                f[0] = byte_f32<0>(lo); f[2] = byte_f32<1>(lo); f[4] = byte_f32<2>(lo); f[6] = byte_f32<3>(lo);
-                f[1] = byte_f32<0>(hi); f[3] = byte_f32<1>(hi); f[5] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
+                lo = raw[0][c] & 0x0F0F0F0Fu;
+                hi = (raw[0][c] >> 4) & 0x0F0F0F0Fu;
             }
+            constexpr bool kPairs = WF == WF_AFFINE4;
+            f[0] = byte_f32<0>(lo); f[kPairs ? 2 : 1] = byte_f32<1>(lo); f[kPairs ? 4 : 2] = byte_f32<2>(lo); f[kPairs ? 6 : 3] = byte_f32<3>(lo);
+            f[kPairs ? 1 : 4] = byte_f32<0>(hi); f[kPairs ? 3 : 5] = byte_f32<1>(hi); f[kPairs ? 5 : 6] = byte_f32<2>(hi); f[7] = byte_f32<3>(hi);
 #pragma unroll
             for (int e = 0; e < 8; e++) f[e] = sc[t](f[e]);
             *reinterpret_cast<u32x4_t*>(out + (c >> 1) * kUnit + (c & 1) * 512) = pack8(DT_F16, f);
@@ -170,7 +187,8 @@ template <int WF>
 static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, uint8_t* img,
                                  hipStream_t s) {
     if (!transposed) {
-        const int64_t kgroups = (K + 1023) / 1024, blocks = (N + 31) / 32 * mats * kgroups;
+        constexpr int kGroupK = WF == WF_AFFINE8 ? 512 : 1024;
+        const int64_t kgroups = (K + kGroupK - 1) / kGroupK, blocks = (N + 31) / 32 * mats * kgroups;
         if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
         hipLaunchKernelGGL((k_pack_weights<WF>), dim3((unsigned)blocks), dim3(256), 0, s, w[0], w[mats - 1], mats, (int)N, K,
                            image_slices(K), kgroups, img);
@@ -306,71 +324,87 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_dz(const LinearGradArgs a
     const int64_t row = (m < a.M ? m : a.M - 1) * a.N, chunks = slices * 2;      // of one projection, padded
     float dz[2][8], mx = 0.0f;
     auto left_of = [&](int64_t c) { return (int)(a.N - c * 8 < 8 ? a.N - c * 8 : 8); };
+    // The exponent of the row's largest |dz| needs all of dz first.  Instead of
+    // computing it twice, the largest |dy| gives a guess (to 2^8) that holds if
+    // the largest |dz| then lies in [2^-2, 2^15), where binary16 keeps its bits;
+    // the rows that miss it write the image again.
     for (int64_t c = c0; c * 8 < a.N; c += kPackThreads / 8) {
-        load_dz<VEC>(a, row + c * 8, left_of(c), dz);
+        unpack8(DT_BF16, load8_raw<VEC>(a.dy, row + c * 8, left_of(c)), dz[0]);
         mx = max8(dz[0], mx);
-        if (a.nmat == 2) mx = max8(dz[1], mx);
     }
-    const int e = row_exponent(rows_max(mx, red));
-    const float scale = ldexpf(1.0f, e);
+    const bool exact = !a.pre[0];                            // dz is dy
+    int e = row_exponent(rows_max(mx, red));
+    if (!exact) e = e - 7 < -113 ? -113 : e - 7;
     const bool live = m < a.M;
-    for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
-        const int left = left_of(c);
-        load_dz<VEC>(a, row + (left > 0 ? c * 8 : 0), left, dz);
+    for (bool again = false;; again = true) {
+        const float scale = ldexpf(1.0f, e);
+        mx = 0.0f;
+        for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+            const int left = left_of(c);
+            load_dz<VEC>(a, row + (left > 0 ? c * 8 : 0), left, dz);
+            mx = max8(dz[0], mx);
+            if (a.nmat == 2) mx = max8(dz[1], mx);
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            if (i >= a.nmat) break;
-            float v[8];
+            for (int i = 0; i < 2; i++) {
+                if (i >= a.nmat) break;
+                float v[8];
 #pragma unroll
-            for (int t = 0; t < 8; t++) v[t] = dz[i][t];
-            if (live) {
-                if (a.dz[i] && left > 0) store8<VEC>(a.dz[i], row + c * 8, left, pack8(DT_BF16, v));
-                float sv[8];
+                for (int t = 0; t < 8; t++) v[t] = dz[i][t];
+                if (live) {
+                    if (a.dz[i] && left > 0 && !again) store8<VEC>(a.dz[i], row + c * 8, left, pack8(DT_BF16, v));
+                    float sv[8];
 #pragma unroll
-                for (int t = 0; t < 8; t++) sv[t] = v[t] * scale;
-                *reinterpret_cast<u32x4_t*>(piece(img, m, slices * a.nmat, c + i * chunks)) = pack8(DT_F16, sv);
-            }
-            if (a.dbias[i]) {
-#pragma unroll
-                for (int t = 0; t < 8; t++) {
-                    float q = live ? v[t] : 0.0f;
-                    q += __shfl_xor(q, 1, 64);
-                    q += __shfl_xor(q, 2, 64);
-                    q += __shfl_xor(q, 4, 64);
-                    v[t] = q;
+                    for (int t = 0; t < 8; t++) sv[t] = v[t] * scale;
+                    *reinterpret_cast<u32x4_t*>(piece(img, m, slices * a.nmat, c + i * chunks)) = pack8(DT_F16, sv);
                 }
-                // lane r of the eight stores column c * 8 + r
-                float mine = v[0];
+                if (a.dbias[i] && !again) {
 #pragma unroll
-                for (int t = 1; t < 8; t++) mine = (lane & 7) == t ? v[t] : mine;
-                if ((lane & 7) < left) sums[((int64_t)blockIdx.x * a.nmat + i) * a.N + c * 8 + (lane & 7)] = mine;
+                    for (int t = 0; t < 8; t++) {
+                        float q = live ? v[t] : 0.0f;
+                        q += __shfl_xor(q, 1, 64);
+                        q += __shfl_xor(q, 2, 64);
+                        q += __shfl_xor(q, 4, 64);
+                        v[t] = q;
+                    }
+                    // lane r of the eight stores column c * 8 + r
+                    float mine = v[0];
+#pragma unroll
+                    for (int t = 1; t < 8; t++) mine = (lane & 7) == t ? v[t] : mine;
+                    if ((lane & 7) < left) sums[((int64_t)blockIdx.x * a.nmat + i) * a.N + c * 8 + (lane & 7)] = mine;
+                }
             }
         }
+        if (exact || again) break;
+        __syncthreads();                                     // `red` is read no more
+        mx = rows_max(mx, red);
+        const int at = mx > 0.0f && mx <= 3.4028234663852886e38f ? __builtin_amdgcn_frexp_expf(mx) - 1 + e : 0;
+        const bool miss = at < -2 || at >= 15;
+        if (miss) e = row_exponent(mx);
+        if (!__syncthreads_or(miss)) break;
     }
     if (threadIdx.x < 8 && live) xexp[m] = (int8_t)e;
 }
 
 // Columns of the sums of row groups, in order: a workgroup takes 64 columns of a
-// projection, its four waves a quarter of the groups each.
-__global__ __launch_bounds__(256) void k_join_sums(const float* __restrict__ sums, int64_t groups, int nmat, int64_t N,
-                                                   float* __restrict__ out0, float* __restrict__ out1) {
-    __shared__ float red[4][64];
+// projection, its sixteen waves a sixteenth of the groups each.
+__global__ __launch_bounds__(1024) void k_join_sums(const float* __restrict__ sums, int64_t groups, int nmat, int64_t N,
+                                                    float* __restrict__ out0, float* __restrict__ out1) {
+    __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.y;
     const int64_t n = (int64_t)blockIdx.x * 64 + lane;
     float* out = i ? out1 : out0;
     if (!out) return;
-    const int64_t g0 = groups * wave / 4, g1 = groups * (wave + 1) / 4;
-    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n < N) {
-        int64_t g = g0;
-        for (; g + 4 <= g1; g += 4)
-#pragma unroll
-            for (int e = 0; e < 4; e++) t[e] += sums[((g + e) * nmat + i) * N + n];
-        for (; g < g1; g++) t[0] += sums[(g * nmat + i) * N + n];
-    }
-    red[wave][lane] = (t[0] + t[1]) + (t[2] + t[3]);
+    const int64_t last = groups * (wave + 1) / 16;
+    float t = 0.0f;
+    if (n < N)
+#pragma unroll 8
+        for (int64_t g = groups * wave / 16; g < last; g++) t += sums[(g * nmat + i) * N + n];
+    red[wave][lane] = t;
     __syncthreads();
-    if (wave == 0 && n < N) out[n] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+    if (wave == 0 && n < N) {
+        for (int w = 1; w < 16; w++) t += red[w][lane];
+        out[n] = t;
+    }
 }
 
 int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N) { return (M + 7) / 8 * nmat * N * 4; }
@@ -380,7 +414,7 @@ hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, f
     auto k = a.N % 8 == 0 ? k_pack_dz<true> : k_pack_dz<false>;
     hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(kPackThreads), 0, s, a, image_slices(a.N), img, xexp, sums);
     if (a.dbias[0] || a.dbias[1])
-        hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(256), 0, s, sums, groups, a.nmat,
+        hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(1024), 0, s, sums, groups, a.nmat,
                            a.N, a.dbias[0], a.dbias[1]);
     return hipGetLastError();
 }

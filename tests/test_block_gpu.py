@@ -209,6 +209,35 @@ def test_gated_backward(fmt, M, N, K):
         near(out["dup_bias"], dbu, F32, "dup_bias")
 
 
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_gradients_of_very_different_rows(M):
+    """Rows of dz far above, far below and at the size of their dy, zero rows, and
+    rows with an infinity or a NaN, which spoil no other row."""
+    gen = torch.Generator().manual_seed(M)
+    N, K = 256, 128
+    (gw, Wg), (uw, Wu) = weight("affine4", N, K, 1), weight("affine4", N, K, 2)
+    rows = torch.arange(M)
+    size = torch.tensor([1.0, 1e-20, 1e12, 1e-30, 0.0])[rows % 5]       # of u, and so of dz against dh
+    dh, _ = rand(gen, M, N, scale=1e-3)
+    dh = (dh.float() * torch.tensor([1.0, 1e8, 1e-20])[rows % 3][:, None].cuda()).bfloat16()
+    g, g64 = rand(gen, M, N)
+    u = (torch.randn(M, N, generator=gen) * size[:, None]).bfloat16().cuda()
+    g[rows.cuda() % 5 != 0] = 0.0                                      # act(0) = 0: dup is zero there, dgate is dh u / 2
+    bad = {1: float("inf"), 2: float("nan")} if M > 2 else {}
+    for m, v in bad.items():
+        dh[m, 3] = v
+    out = Q.q4_gated_backward(gw, uw, dh, g, u)
+    dx, dg, du, _, _ = R.gated_grad(Wg, Wu, dh.double().cpu(), g.double().cpu(), u.double().cpu(), "silu")
+    got = out["dx"].double().cpu()
+    for m in range(M):
+        if m in bad:
+            assert not torch.isfinite(got[m]).any()
+        else:
+            # below 2^-126 values keep an absolute spacing only (2^-133), and flush to zero below that
+            for a, b, limit in ((got[m], dx[m], bar(torch.bfloat16)), (out["dgate"][m].double().cpu(), dg[m], U[torch.bfloat16])):
+                assert (a - b).norm() <= limit * b.norm() + 2.0 ** -132 * b.numel() ** 0.5, m
+
+
 @pytest.mark.parametrize("M", [1, 5, 70])
 def test_product_gradients_against_differences(M):
     """<dx, v> and the bias gradients' <db, v> against central differences of
