@@ -123,15 +123,14 @@ __device__ __forceinline__ void store_elem(void* p, int dt, int64_t i, float v) 
 __device__ __forceinline__ float fast_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504088896f); }
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-v)); }
 
-// act(z), and with GRAD its derivative in `slope`.
-template <bool GRAD>
-__device__ __forceinline__ float activate(int act, float z, float& slope) {
-    if (act == ACT_SILU) {
+// Activation ACT of z, and with GRAD its derivative in `slope`.
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float activate(float z, float& slope) {
+    if constexpr (ACT == ACT_SILU) {
         const float s = sigmoid(z);
         if constexpr (GRAD) slope = fmaf(z, s * (1.0f - s), s);
         return z * s;
-    }
-    if (act == ACT_GELU) {
+    } else if constexpr (ACT == ACT_GELU) {
         const float x = fabsf(z) * 0.707106781186548f;
         const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
         const float e = fast_exp(-x * x);
@@ -143,24 +142,36 @@ __device__ __forceinline__ float activate(int act, float z, float& slope) {
         const float F = z < 0.0f ? q : 1.0f - q;
         if constexpr (GRAD) slope = fmaf(z * 0.398942280401433f, e, F);
         return z * F;
-    }
-    if (act == ACT_GELU_TANH) {
+    } else if constexpr (ACT == ACT_GELU_TANH) {
         constexpr float c = 1.59576912160573f;     // 2 sqrt(2 / pi)
         const float z2 = z * z;
         const float s = sigmoid(c * z * fmaf(0.044715f, z2, 1.0f));
         if constexpr (GRAD) slope = fmaf(z * c * fmaf(0.134145f, z2, 1.0f), s * (1.0f - s), s);
         return z * s;
-    }
-    if (act == ACT_RELU) {
+    } else if constexpr (ACT == ACT_RELU) {
         if constexpr (GRAD) slope = z > 0.0f ? 1.0f : 0.0f;
         return z < 0.0f ? 0.0f : z;        // a NaN stays one
+    } else {
+        if constexpr (GRAD) slope = 1.0f;
+        return z;
     }
-    if constexpr (GRAD) slope = 1.0f;
-    return z;
 }
-__device__ __forceinline__ float activate(int act, float z) {
-    float unused;
-    return activate<false>(act, z, unused);
+// N values at once: one branch on the activation, then independent chains (a
+// branch at every value kept eight exponentials from overlapping).
+template <int ACT, bool GRAD, int N>
+__device__ __forceinline__ void activate_as(const float (&z)[N], float (&v)[N], float (&slope)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; e++) v[e] = activate<ACT, GRAD>(z[e], slope[e]);
+}
+template <bool GRAD, int N>
+__device__ __forceinline__ void activate_all(int act, const float (&z)[N], float (&v)[N], float (&slope)[N]) {
+    switch (act) {
+        case ACT_SILU: activate_as<ACT_SILU, GRAD>(z, v, slope); break;
+        case ACT_GELU: activate_as<ACT_GELU, GRAD>(z, v, slope); break;
+        case ACT_GELU_TANH: activate_as<ACT_GELU_TANH, GRAD>(z, v, slope); break;
+        case ACT_RELU: activate_as<ACT_RELU, GRAD>(z, v, slope); break;
+        default: activate_as<ACT_NONE, GRAD>(z, v, slope);
+    }
 }
 
 }  // namespace q4

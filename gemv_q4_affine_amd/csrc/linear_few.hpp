@@ -524,7 +524,9 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
         float z = sum(GATED ? 2 * p : p);
         if (a.bias[0]) z += load_elem(a.bias[0], XDT, n);
         if (a.pre[0]) store_elem(a.pre[0], XDT, at, z);
-        float y = activate(a.act, z);
+        float zs[1] = {z}, none[1];
+        activate_all<false>(a.act, zs, zs, none);
+        float y = zs[0];
         if constexpr (GATED) {
             float u = sum(2 * p + 1);
             if (a.bias[1]) u += load_elem(a.bias[1], XDT, n);

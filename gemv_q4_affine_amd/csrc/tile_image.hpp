@@ -152,10 +152,7 @@ __device__ __forceinline__ void epilogue8(const EpilogueArgs& a, int64_t m, int6
         }
         if (a.pre[1]) store8<VEC>(a.pre[1], o, left, pack8(a.dtype, z2));
     }
-    if (a.act != ACT_NONE) {
-#pragma unroll
-        for (int e = 0; e < 8; e++) z[e] = activate(a.act, z[e]);
-    }
+    if (a.act != ACT_NONE) activate_all<false>(a.act, z, z, t);
     if constexpr (EPI == EPI_GATED) {
 #pragma unroll
         for (int e = 0; e < 8; e++) z[e] *= z2[e];

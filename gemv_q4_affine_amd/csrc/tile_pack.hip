@@ -216,7 +216,8 @@ hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int
 // values down to 2^-29 of the row's largest keep binary16's 11 bits (bfloat16
 // values: exact).  The product's epilogue takes 2^-e off again.  A workgroup
 // takes eight rows, so that a piece's eight rows are 128 contiguous bytes of
-// the image; it reads them twice, the second time from cache.
+// the image (four where eight would leave CUs idle); it reads them twice, the
+// second time from cache.
 constexpr int kPackThreads = 1024;
 
 __device__ __forceinline__ int row_exponent(float mx) {
@@ -225,16 +226,16 @@ __device__ __forceinline__ int row_exponent(float mx) {
     return e < -113 ? -113 : e > 127 ? 127 : e;
 }
 
-// Maximum over the lanes and waves that hold the same row (lane & 7).
+// Maximum over the lanes and waves that hold the same row (lane % ROWS).
+template <int ROWS>
 __device__ __forceinline__ float rows_max(float mx, float (*red)[8]) {
-    mx = fmaxf(mx, __shfl_xor(mx, 8, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+#pragma unroll
+    for (int d = ROWS; d < 64; d *= 2) mx = fmaxf(mx, __shfl_xor(mx, d, 64));
     const int lane = threadIdx.x & 63;
-    if (lane < 8) red[threadIdx.x >> 6][lane] = mx;
+    if (lane < ROWS) red[threadIdx.x >> 6][lane] = mx;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kPackThreads / 64; w++) mx = fmaxf(mx, red[w][lane & 7]);
+    for (int w = 0; w < kPackThreads / 64; w++) mx = fmaxf(mx, red[w][lane % ROWS]);
     return mx;
 }
 
@@ -248,63 +249,66 @@ __device__ __forceinline__ float max8(const float (&v)[8], float mx) {
     return mx;
 }
 
+template <int ROWS>
 __global__ __launch_bounds__(kPackThreads) void k_pack_rows(const void* __restrict__ x, int dtype, int64_t M, int64_t K,
                                                             int64_t slices, uint8_t* __restrict__ img,
                                                             int8_t* __restrict__ xexp) {
     __shared__ float red[kPackThreads / 64][8];
     const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * 8 + (lane & 7), c0 = (threadIdx.x >> 6) * 8 + (lane >> 3);
+    constexpr int kStride = kPackThreads / ROWS;
+    const int64_t m = (int64_t)blockIdx.x * ROWS + lane % ROWS, c0 = (threadIdx.x >> 6) * (64 / ROWS) + lane / ROWS;
     const int64_t row = (m < M ? m : M - 1) * K, chunks = K / 8;          // K % 32 == 0
     float v[8], mx = 0.0f;
-    for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+    for (int64_t c = c0; c < chunks; c += kStride) {
         unpack8(dtype, load8_raw<true>(x, row + c * 8, 8), v);
         mx = max8(v, mx);
     }
-    const int e = row_exponent(rows_max(mx, red));
+    const int e = row_exponent(rows_max<ROWS>(mx, red));
     const float scale = ldexpf(1.0f, e);
     if (m < M) {
-        for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+        for (int64_t c = c0; c < chunks; c += kStride) {
             unpack8(dtype, load8_raw<true>(x, row + c * 8, 8), v);
 #pragma unroll
             for (int i = 0; i < 8; i++) v[i] *= scale;
             *reinterpret_cast<u32x4_t*>(piece(img, m, slices, c)) = pack8(DT_F16, v);
         }
-        if (threadIdx.x < 8) xexp[m] = (int8_t)e;
+        if (threadIdx.x < ROWS) xexp[m] = (int8_t)e;
     }
 }
 
+// Rows of a workgroup: four where eight would leave CUs idle.
+static int pack_rows(int64_t M) { return M > 8 * 256 - 8 ? 8 : 4; }
+
 hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, uint8_t* img, int8_t* xexp, hipStream_t s) {
-    hipLaunchKernelGGL(k_pack_rows, dim3((unsigned)((M + 7) / 8)), dim3(kPackThreads), 0, s, x, dtype, M, K,
-                       image_slices(K), img, xexp);
+    const int rows = pack_rows(M);
+    hipLaunchKernelGGL(rows == 8 ? k_pack_rows<8> : k_pack_rows<4>, dim3((unsigned)((M + rows - 1) / rows)),
+                       dim3(kPackThreads), 0, s, x, dtype, M, K, image_slices(K), img, xexp);
     return hipGetLastError();
 }
 
 // dz of the projections: the same image (the projections' slices follow each
 // other), the dz outputs rounded from the same binary32 values, and the sums of
-// the workgroup's eight rows, joined by k_join_sums in a fixed order.
+// the workgroup's rows, joined by k_join_sums in a fixed order.
 template <bool VEC>
 __device__ __forceinline__ void load_dz(const LinearGradArgs& a, int64_t o, int left, float (&dz)[2][8]) {
     unpack8(DT_BF16, load8_raw<VEC>(a.dy, o, left), dz[0]);
     if (a.pre[0]) {
-        float g[8];
+        float g[8], slope[8];
         unpack8(DT_BF16, load8_raw<VEC>(a.pre[0], o, left), g);
         if (a.nmat == 2) {
             float u[8];
             unpack8(DT_BF16, load8_raw<VEC>(a.pre[1], o, left), u);
+            activate_all<true>(a.act, g, g, slope);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                float slope;
-                const float v = activate<true>(a.act, g[e], slope), dh = dz[0][e];
-                dz[0][e] = dh * u[e] * slope;
-                dz[1][e] = dh * v;
+                const float dh = dz[0][e];
+                dz[0][e] = dh * u[e] * slope[e];
+                dz[1][e] = dh * g[e];
             }
         } else {
+            activate_all<true>(a.act, g, g, slope);
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                float slope;
-                activate<true>(a.act, g[e], slope);
-                dz[0][e] *= slope;
-            }
+            for (int e = 0; e < 8; e++) dz[0][e] *= slope[e];
         }
     }
     // past the row's end: zeros in the image, whatever the derivative of zeros is
@@ -315,12 +319,13 @@ __device__ __forceinline__ void load_dz(const LinearGradArgs& a, int64_t o, int 
     }
 }
 
-template <bool VEC>
+template <bool VEC, int ROWS>
 __global__ __launch_bounds__(kPackThreads) void k_pack_dz(const LinearGradArgs a, int64_t slices, uint8_t* __restrict__ img,
                                                           int8_t* __restrict__ xexp, float* __restrict__ sums) {
     __shared__ float red[kPackThreads / 64][8];
     const int lane = threadIdx.x & 63;
-    const int64_t m = (int64_t)blockIdx.x * 8 + (lane & 7), c0 = (threadIdx.x >> 6) * 8 + (lane >> 3);
+    constexpr int kStride = kPackThreads / ROWS;
+    const int64_t m = (int64_t)blockIdx.x * ROWS + lane % ROWS, c0 = (threadIdx.x >> 6) * (64 / ROWS) + lane / ROWS;
     const int64_t row = (m < a.M ? m : a.M - 1) * a.N, chunks = slices * 2;      // of one projection, padded
     float dz[2][8], mx = 0.0f;
     auto left_of = [&](int64_t c) { return (int)(a.N - c * 8 < 8 ? a.N - c * 8 : 8); };
@@ -328,18 +333,18 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_dz(const LinearGradArgs a
     // computing it twice, the largest |dy| gives a guess (to 2^8) that holds if
     // the largest |dz| then lies in [2^-2, 2^15), where binary16 keeps its bits;
     // the rows that miss it write the image again.
-    for (int64_t c = c0; c * 8 < a.N; c += kPackThreads / 8) {
+    for (int64_t c = c0; c * 8 < a.N; c += kStride) {
         unpack8(DT_BF16, load8_raw<VEC>(a.dy, row + c * 8, left_of(c)), dz[0]);
         mx = max8(dz[0], mx);
     }
     const bool exact = !a.pre[0];                            // dz is dy
-    int e = row_exponent(rows_max(mx, red));
+    int e = row_exponent(rows_max<ROWS>(mx, red));
     if (!exact) e = e - 7 < -113 ? -113 : e - 7;
     const bool live = m < a.M;
     for (bool again = false;; again = true) {
         const float scale = ldexpf(1.0f, e);
         mx = 0.0f;
-        for (int64_t c = c0; c < chunks; c += kPackThreads / 8) {
+        for (int64_t c = c0; c < chunks; c += kStride) {
             const int left = left_of(c);
             load_dz<VEC>(a, row + (left > 0 ? c * 8 : 0), left, dz);
             mx = max8(dz[0], mx);
@@ -361,28 +366,31 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_dz(const LinearGradArgs a
 #pragma unroll
                     for (int t = 0; t < 8; t++) {
                         float q = live ? v[t] : 0.0f;
-                        q += __shfl_xor(q, 1, 64);
-                        q += __shfl_xor(q, 2, 64);
-                        q += __shfl_xor(q, 4, 64);
+#pragma unroll
+                        for (int d = 1; d < ROWS; d *= 2) q += __shfl_xor(q, d, 64);
                         v[t] = q;
                     }
-                    // lane r of the eight stores column c * 8 + r
-                    float mine = v[0];
+                    // lane r of the rows stores columns c * 8 + r, + ROWS ..
 #pragma unroll
-                    for (int t = 1; t < 8; t++) mine = (lane & 7) == t ? v[t] : mine;
-                    if ((lane & 7) < left) sums[((int64_t)blockIdx.x * a.nmat + i) * a.N + c * 8 + (lane & 7)] = mine;
+                    for (int t0 = 0; t0 < 8; t0 += ROWS) {
+                        float mine = v[t0];
+#pragma unroll
+                        for (int t = 1; t < ROWS; t++) mine = lane % ROWS == t ? v[t0 + t] : mine;
+                        const int col = t0 + lane % ROWS;
+                        if (col < left) sums[((int64_t)blockIdx.x * a.nmat + i) * a.N + c * 8 + col] = mine;
+                    }
                 }
             }
         }
         if (exact || again) break;
         __syncthreads();                                     // `red` is read no more
-        mx = rows_max(mx, red);
+        mx = rows_max<ROWS>(mx, red);
         const int at = mx > 0.0f && mx <= 3.4028234663852886e38f ? __builtin_amdgcn_frexp_expf(mx) - 1 + e : 0;
         const bool miss = at < -2 || at >= 15;
         if (miss) e = row_exponent(mx);
         if (!__syncthreads_or(miss)) break;
     }
-    if (threadIdx.x < 8 && live) xexp[m] = (int8_t)e;
+    if (threadIdx.x < ROWS && live) xexp[m] = (int8_t)e;
 }
 
 // Columns of the sums of row groups, in order: a workgroup takes 64 columns of a
@@ -407,11 +415,13 @@ __global__ __launch_bounds__(1024) void k_join_sums(const float* __restrict__ su
     }
 }
 
-int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N) { return (M + 7) / 8 * nmat * N * 4; }
+int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N) { return (M + pack_rows(M) - 1) / pack_rows(M) * nmat * N * 4; }
 
 hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s) {
-    const int64_t groups = (a.M + 7) / 8;
-    auto k = a.N % 8 == 0 ? k_pack_dz<true> : k_pack_dz<false>;
+    const int rows = pack_rows(a.M);
+    const int64_t groups = (a.M + rows - 1) / rows;
+    auto k = a.N % 8 == 0 ? (rows == 8 ? k_pack_dz<true, 8> : k_pack_dz<true, 4>)
+                          : (rows == 8 ? k_pack_dz<false, 8> : k_pack_dz<false, 4>);
     hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(kPackThreads), 0, s, a, image_slices(a.N), img, xexp, sums);
     if (a.dbias[0] || a.dbias[1])
         hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(1024), 0, s, sums, groups, a.nmat,
