@@ -8,8 +8,9 @@ namespace q4 {
 namespace {
 
 // Rows that the few-row kernel takes, in two launches above its own 32: the
-// weights are streamed twice, but not written as an image (12288 x 4096, 33 to 64
-// rows: 2 x 21 us against 30 for the image and 22 for its product).
+// weights are streamed twice, but not written as an image (Q4_0, 64 rows: 12288 x
+// 4096 2 x 21 us against 57, of which 23 for the image and 21 for its product; 4096 x
+// 14336 2 x 23 + 5 against 80; 2048 x 2048, 33 rows, 14 against 22).
 constexpr int64_t kFewCallMaxM = 2 * kFewMaxM;
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -55,29 +56,93 @@ TileArgs tile_args(const Layout& l, uint8_t* ws) {
 
 }  // namespace
 
-int64_t linear_workspace_bytes(int, int nmat, int64_t M, int64_t N, int64_t K) {
-    return M <= kFewCallMaxM ? 0 : forward_layout(nmat, M, N, K).total;
+// A workgroup reads all of x that its steps meet, so one that has few column
+// tiles and a long K is bound by x, and few workgroups leave CUs idle.  Above
+// four rows a K of 32 steps or more is split into parts of 8 steps at least, to
+// two workgroups a CU at most, and joined (about 4 us): 4096 x 14336, 32 rows,
+// 38.7 us whole against 23.9 + 3.9 in 4 parts (16 rows 22.4, 16.2 + 3.9); 512 x
+// 12288 26.2 against 7.8 + 4.8.  Not split: 2048 x 2048 (8 steps) 7.5, in 4 parts
+// 7.1 + 3.6; 8192 x 4096 (16 steps) 15.6, in 2 15.2 + 4.0; up to four rows, where
+// x is small (512 x 12288, one row: 7.4, in 4 parts 4.9 + 2.2).
+//
+// Column tiles of a workgroup: one pair at q4_gated (12288 x 4096: 17.6 us at
+// one row against 18.1 with three pairs, 41.0 at 32 rows against 42.7 with two).
+// At q4_linear two where they fill the CUs (8192 x 4096, 32 rows: 15.6 against 19.2
+// with one; 512 x 12288 in 8 parts: 9.0, with one 7.8), three up to four rows.
+// Eight waves where the workgroups do not outnumber the CUs (4096 x 4096 gated, 32
+// rows: 16.4 against 20.8 with four).
+FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
+    const int64_t step = wf == WF_AFFINE8 ? 128 : 256, steps = (K + step - 1) / step;
+    const int64_t tiles = (N + 15) / 16, cus = current_cu_count(), pairs = (tiles + 1) / 2;
+    const int64_t most = M > 4 && steps >= 32 ? steps / 8 : 1;
+    FewPlan p{};
+    p.tiles = nmat == 2 || (most > 1 ? pairs * most < cus : tiles <= cus) ? 1 : tiles <= 2 * cus || M > 4 ? 2 : 3;
+    const int64_t groups = (tiles + p.tiles - 1) / p.tiles, room = 2 * cus / groups;
+    const int64_t parts = room < 1 ? 1 : room < most ? room : most;
+    p.per = (int)((steps + parts - 1) / parts);
+    p.parts = (int)((steps + p.per - 1) / p.per);
+    p.waves = M <= 4 || groups * p.parts <= cus ? 8 : 4;
+    return p;
+}
+
+static int64_t few_rows_of(int64_t M) { return M <= kFewMaxM ? M : (M + 1) / 2; }
+static int64_t few_part_row(int nmat, int64_t N) { return (N + 31) / 32 * nmat * 32; }
+
+int64_t linear_workspace_bytes(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
+    if (M > kFewCallMaxM) return forward_layout(nmat, M, N, K).total;
+    const FewPlan p = plan_few(wf, nmat, few_rows_of(M), N, K);
+    return p.parts > 1 ? p.parts * M * few_part_row(nmat, N) * 4 : 0;
 }
 
 // The few-row kernel on rows m0 .. m0 + count - 1.
-static hipError_t launch_few(const LinearArgs& a, int64_t m0, int64_t count, hipStream_t s) {
+static hipError_t launch_few(const LinearArgs& a, const FewPlan& p, int64_t m0, int64_t count, float* part, hipStream_t s) {
     LinearArgs t = a;
-    auto rows = [&](const void* p, int64_t width) {
-        return p ? const_cast<char*>(static_cast<const char*>(p)) + m0 * width * 2 : nullptr;
+    auto rows = [&](const void* v, int64_t width) {
+        return v ? const_cast<char*>(static_cast<const char*>(v)) + m0 * width * 2 : nullptr;
     };
     t.M = count;
     t.x = rows(a.x, a.K);
     t.y = rows(a.y, a.N);
     t.residual = rows(a.residual, a.N);
     for (int i = 0; i < 2; i++) t.pre[i] = rows(a.pre[i], a.N);
-    return t.wf == WF_Q4_0 ? launch_few_q4_0(t, s) : t.wf == WF_AFFINE4 ? launch_few_affine4(t, s) : launch_few_affine8(t, s);
+    FewSplit split{};
+    split.rows = a.M;
+    split.np = few_part_row(a.nmat, a.N);
+    split.part = p.parts > 1 ? part + m0 * split.np : nullptr;
+    return t.wf == WF_Q4_0      ? launch_few_q4_0(t, p, split, s)
+           : t.wf == WF_AFFINE4 ? launch_few_affine4(t, p, split, s)
+                                : launch_few_affine8(t, p, split, s);
+}
+
+static EpilogueArgs epilogue_args(const LinearArgs& a) {
+    EpilogueArgs e{};
+    e.act = a.act;
+    e.dtype = a.dtype;
+    e.M = a.M;
+    e.N = a.N;
+    for (int i = 0; i < 2; i++) {
+        e.bias[i] = a.bias[i];
+        e.pre[i] = a.pre[i];
+    }
+    e.residual = a.residual;
+    e.y = a.y;
+    return e;
 }
 
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
     if (a.M <= kFewCallMaxM) {
-        const int64_t first = a.M <= kFewMaxM ? a.M : (a.M + 1) / 2;
-        const hipError_t e = launch_few(a, 0, first, s);
-        return e != hipSuccess || first == a.M ? e : launch_few(a, first, a.M - first, s);
+        const int64_t first = few_rows_of(a.M);
+        const FewPlan p = plan_few(a.wf, a.nmat, first, a.N, a.K);
+        float* part = static_cast<float*>(workspace);
+        hipError_t e = launch_few(a, p, 0, first, part, s);
+        if (e == hipSuccess && first < a.M) e = launch_few(a, p, first, a.M - first, part, s);
+        if (e != hipSuccess || p.parts == 1) return e;
+        TileArgs t{};
+        t.part = part;
+        t.parts = p.parts;
+        t.w_panels = (a.N + 31) / 32 * a.nmat;
+        t.epi = epilogue_args(a);
+        return launch_tile_join(a.nmat, t, s);
     }
     const Layout l = forward_layout(a.nmat, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -86,16 +151,7 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
         e = launch_pack_x(a.x, a.dtype, a.M, a.K, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at), s);
     if (e != hipSuccess) return e;
     TileArgs t = tile_args(l, ws);
-    t.epi.act = a.act;
-    t.epi.dtype = a.dtype;
-    t.epi.M = a.M;
-    t.epi.N = a.N;
-    for (int i = 0; i < 2; i++) {
-        t.epi.bias[i] = a.bias[i];
-        t.epi.pre[i] = a.pre[i];
-    }
-    t.epi.residual = a.residual;
-    t.epi.y = a.y;
+    t.epi = epilogue_args(a);
     return launch_tile_gemm(l.plan, a.nmat, t, s);
 }
 

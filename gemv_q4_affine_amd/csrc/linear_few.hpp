@@ -35,7 +35,8 @@
 //
 // The waves of a workgroup take steps in turn, each its next one in flight while
 // it multiplies, and add their sums through LDS in wave order (deterministic).
-// For q4_gated the tiles come in pairs, gate and up of the same 16 columns.
+// For q4_gated the tiles come in pairs, gate and up of the same 16 columns.  A
+// long sum over few columns is split over workgroups (FewSplit) and joined.
 //
 // Bound: memory at 1 to 16 rows (each weight byte is read once).  Measured, Q4_0,
 // N = 12288, K = 4096: one row 9.5 us (28.3 MB; with no loads at all 4.4), 16
@@ -120,19 +121,25 @@ __device__ __forceinline__ u32x4_t bytes8(uint32_t lo, uint32_t hi) {
 
 }  // namespace few
 
-constexpr int kFewMaxM = 32;
+// A sum split over workgroups: part blockIdx.y takes `per` steps and leaves its
+// sums in rows of `np` values (the order of k_tile_join), unrounded.
+struct FewSplit {
+    float* part;          // null: one part, the epilogue here
+    int64_t rows, np;     // rows of a part (of the whole call)
+    int per, x_shift;
+};
 
-// Waves and LDS of a variant.  Up to four rows eight waves share a CU's LDS
-// (their steps are what is in flight); with more rows x takes its place.
-template <int MT, bool DIAG> constexpr int few_waves() { return DIAG ? 8 : 4; }
-constexpr int kFewX = 32 << 10;              // x
+// Waves and LDS of a variant.  What is in flight on a CU is a step a wave: up to
+// four rows a workgroup has eight waves, above them four, so that two workgroups
+// with their x share a CU, or eight where there is but one workgroup a CU.
+template <int WAVES, bool DIAG> constexpr int few_x() { return DIAG ? 32 << 10 : WAVES << 13; }      // x
 
-template <int WF, int XDT, int MT, int NT, bool GATED, bool DIAG>
-__global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const LinearArgs a, int x_shift) {
+template <int WF, int XDT, int MT, int NT, bool GATED, bool DIAG, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a, const FewSplit split) {
     using namespace few;
     static_assert(!DIAG || MT == 1, "a form for few rows");
     constexpr bool kBlocks = DIAG && WF != WF_AFFINE8;       // the block-diagonal x (see above)
-    constexpr int kMaxWaves = few_waves<MT, DIAG>(), kX = kFewX;
+    constexpr int kMaxWaves = WAVES, kX = few_x<WAVES, DIAG>();
     constexpr int kTile = DIAG ? 4 * 16 : MT * 16 * 16;
     constexpr int kStepB = 2048, kScaleB = 256;              // codes and scales of a tile and step
     constexpr int kStep = WF == WF_AFFINE8 ? 128 : 256;      // weights of a row and step
@@ -142,10 +149,11 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
     uint8_t* xs = lds + kRing + kScales;
     float* red = reinterpret_cast<float*>(lds);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6, x_rows = 1 << x_shift;
+    const int waves = blockDim.x >> 6, x_shift = split.x_shift, x_rows = 1 << x_shift;
     const int j = lane & 15, g = lane >> 4;
     const int K = (int)a.K, N = (int)a.N, M = (int)a.M;
-    const int nb = K / 32, steps = (K + kStep - 1) / kStep;
+    const int nb = K / 32, s0 = (int)blockIdx.y * split.per, left_steps = (K + kStep - 1) / kStep - s0;
+    const int steps = left_steps < split.per ? left_steps : split.per;     // of this part, counted from s0
     constexpr int kCols = GATED ? NT / 2 : NT;              // column tiles of 16 outputs
     const int n0 = (int)blockIdx.x * kCols * 16;
 
@@ -172,7 +180,7 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const uint32_t row = copy_row[h] < (uint32_t)in ? copy_row[h] : (uint32_t)in;
-                const uint32_t p = (uint32_t)step * 8u + ((uint32_t)(lane & 7) ^ (copy_row[h] & 7u)), last = row_q / 16 - 1;
+                const uint32_t p = (uint32_t)(s0 + step) * 8u + ((uint32_t)(lane & 7) ^ (copy_row[h] & 7u)), last = row_q / 16 - 1;
                 copy_unit(base, row * row_q + (p < last ? p : last) * 16u, lds0 + t * kStepB + h * 1024);
             }
         }
@@ -185,24 +193,24 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
             n = n < N ? n : N - 1;
             const int64_t at = (int64_t)n * row_s;
             constexpr int kPer = WF == WF_Q4_0 ? 8 : kStep / 64;        // scales of a row and step
-            const int s0 = step * kPer;
-            if (s0 + kPer <= (int)row_s) {
+            const int first = (s0 + step) * kPer;
+            if (first + kPer <= (int)row_s) {
                 if constexpr (WF == WF_Q4_0) {
-                    sc[e] = *reinterpret_cast<const u32x4_u*>(w.s + at + s0);
+                    sc[e] = *reinterpret_cast<const u32x4_u*>(w.s + at + first);
                 } else if constexpr (WF == WF_AFFINE4) {
-                    const u32x2_t s = *reinterpret_cast<const u32x2_u*>(w.s + at + s0), b = *reinterpret_cast<const u32x2_u*>(w.b + at + s0);
+                    const u32x2_t s = *reinterpret_cast<const u32x2_u*>(w.s + at + first), b = *reinterpret_cast<const u32x2_u*>(w.b + at + first);
                     sc[e] = u32x4_t{s[0], s[1], b[0], b[1]};
                 } else {
-                    sc[e] = u32x4_t{*reinterpret_cast<const u32_u*>(w.s + at + s0), 0u, *reinterpret_cast<const u32_u*>(w.b + at + s0), 0u};
+                    sc[e] = u32x4_t{*reinterpret_cast<const u32_u*>(w.s + at + first), 0u, *reinterpret_cast<const u32_u*>(w.b + at + first), 0u};
                 }
             } else {
                 // the last step of a K that is no multiple of it: one by one, zeros past the end
                 u32x4_t v = {0u, 0u, 0u, 0u};
 #pragma unroll
                 for (int i = 0; i < kPer; i++)
-                    if (s0 + i < (int)row_s) {
-                        v[i >> 1] |= (uint32_t)w.s[at + s0 + i] << (16 * (i & 1));
-                        if constexpr (WF != WF_Q4_0) v[2 + (i >> 1)] |= (uint32_t)w.b[at + s0 + i] << (16 * (i & 1));
+                    if (first + i < (int)row_s) {
+                        v[i >> 1] |= (uint32_t)w.s[at + first + i] << (16 * (i & 1));
+                        if constexpr (WF != WF_Q4_0) v[2 + (i >> 1)] |= (uint32_t)w.b[at + first + i] << (16 * (i & 1));
                     }
                 sc[e] = v;
             }
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
     // Piece u of that order, of chunk c: its load, and its place. ----
     auto x_piece = [&](int c, int u) __attribute__((always_inline)) {
         const uint16_t* x = static_cast<const uint16_t*>(a.x);
-        const int gg = u & 3, m = (u >> 2) & (x_rows - 1), b = 4 * c + ((u >> (2 + x_shift)) & 3);     // block of 32
+        const int gg = u & 3, m = (u >> 2) & (x_rows - 1), b = 4 * (s0 * (kStep / 128) + c) + ((u >> (2 + x_shift)) & 3);     // block of 32
         u32x4_t v = {0u, 0u, 0u, 0u};
         if (b < nb) {
             const uint16_t* p = x + (int64_t)(m < M ? m : M - 1) * K;
@@ -412,7 +420,7 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
             early[e] = x_piece(u >> piece_shift, u);
         }
         __builtin_amdgcn_sched_barrier(0);
-        request(wave);                                       // waves <= steps
+        if (wave < steps) request(wave);         // a copy that nobody waits for would land in the sums
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int e = 0; e < kEarly; e++) {
@@ -462,7 +470,7 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
             __syncthreads();
         };
         x_request(0, 0);
-        request(wave);
+        if (wave < steps) request(wave);
         for (int r = 0; r * waves < steps; r++) {
             const int step = r * waves + wave;
             Codes w[kChunks][NT];
@@ -522,6 +530,12 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
         };
         const int64_t at = (int64_t)m * N + n;
         float z = sum(GATED ? 2 * p : p);
+        if (split.part) {
+            float* row = split.part + ((int64_t)blockIdx.y * split.rows + m) * split.np;
+            row[GATED ? (n >> 5) * 64 + (n & 31) : n] = z;
+            if constexpr (GATED) row[(n >> 5) * 64 + 32 + (n & 31)] = sum(2 * p + 1);
+            continue;
+        }
         if (a.bias[0]) z += load_elem(a.bias[0], XDT, n);
         if (a.pre[0]) store_elem(a.pre[0], XDT, at, z);
         float zs[1] = {z}, none[1];
@@ -540,44 +554,52 @@ __global__ __launch_bounds__(DIAG ? 512 : 256, 2) void k_linear_few(const Linear
 
 // ---- host ------------------------------------------------------------------------
 
+constexpr int kFewMaxM = 32;
+
+// Column tiles (at q4_gated pairs) of a workgroup, its waves, the parts of a sum
+// and the steps of a part.
+struct FewPlan {
+    int tiles, waves, parts, per;
+};
+FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K);
+
+template <int WF, int XDT, int MT, int P, bool GATED, bool DIAG, int WAVES>
+void few_launch(const LinearArgs& a, const FewPlan& plan, FewSplit split, hipStream_t s) {
+    split.x_shift = 0;
+    while ((1 << split.x_shift) < a.M) split.x_shift++;
+    split.per = plan.per;
+    const dim3 grid((unsigned)((a.N + 16 * P - 1) / (16 * P)), (unsigned)plan.parts);
+    hipLaunchKernelGGL((k_linear_few<WF, XDT, MT, GATED ? 2 * P : P, GATED, DIAG, WAVES>), grid,
+                       dim3(64 * (unsigned)(plan.per < WAVES ? plan.per : WAVES)), 0, s, a, split);
+}
 template <int WF, int XDT, int MT, int P, bool GATED, bool DIAG>
-void few_launch(const LinearArgs& a, hipStream_t s) {
-    constexpr int kStep = WF == WF_AFFINE8 ? 128 : 256;
-    const int64_t steps = (a.K + kStep - 1) / kStep, most = few_waves<MT, DIAG>();
-    int x_shift = 0;
-    while ((1 << x_shift) < a.M) x_shift++;
-    const unsigned grid = (unsigned)((a.N + 16 * P - 1) / (16 * P));
-    hipLaunchKernelGGL((k_linear_few<WF, XDT, MT, GATED ? 2 * P : P, GATED, DIAG>), dim3(grid),
-                       dim3(64 * (unsigned)(steps < most ? steps : most)), 0, s, a, x_shift);
+void few_waves(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
+    if (DIAG || p.waves == 8) few_launch<WF, XDT, MT, P, GATED, DIAG, 8>(a, p, split, s);
+    else few_launch<WF, XDT, MT, P, GATED, DIAG, DIAG ? 8 : 4>(a, p, split, s);
 }
 template <int WF, int XDT, int MT, bool DIAG>
-void few_tiles(const LinearArgs& a, hipStream_t s) {
-    // Column tiles of a workgroup: as few as fill the CUs, since every workgroup
-    // reads all of x; one pair at q4_gated (12288 x 4096: 17.6 us at one row
-    // against 18.1 with three pairs, 41.0 at 32 rows against 42.7 with two),
-    // at most two tiles above four rows (registers)
-    const int64_t tiles = (a.N + 15) / 16, cus = current_cu_count();
-    if (a.nmat == 2) few_launch<WF, XDT, MT, 1, true, DIAG>(a, s);
-    else if (tiles <= cus) few_launch<WF, XDT, MT, 1, false, DIAG>(a, s);
-    else if (tiles <= 2 * cus || !DIAG) few_launch<WF, XDT, MT, 2, false, DIAG>(a, s);
-    else few_launch<WF, XDT, MT, DIAG ? 3 : 2, false, DIAG>(a, s);
+void few_tiles(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
+    if (a.nmat == 2) few_waves<WF, XDT, MT, 1, true, DIAG>(a, p, split, s);
+    else if (p.tiles == 1) few_waves<WF, XDT, MT, 1, false, DIAG>(a, p, split, s);
+    else if (p.tiles == 2 || !DIAG) few_waves<WF, XDT, MT, 2, false, DIAG>(a, p, split, s);
+    else few_waves<WF, XDT, MT, DIAG ? 3 : 2, false, DIAG>(a, p, split, s);
 }
 template <int WF, int XDT>
-void few_rows(const LinearArgs& a, hipStream_t s) {
-    if (a.M <= 4) few_tiles<WF, XDT, 1, true>(a, s);
-    else if (a.M <= 16) few_tiles<WF, XDT, 1, false>(a, s);
-    else few_tiles<WF, XDT, 2, false>(a, s);
+void few_rows(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
+    if (a.M <= 4) few_tiles<WF, XDT, 1, true>(a, p, split, s);
+    else if (a.M <= 16) few_tiles<WF, XDT, 1, false>(a, p, split, s);
+    else few_tiles<WF, XDT, 2, false>(a, p, split, s);
 }
 template <int WF>
-hipError_t few_format(const LinearArgs& a, hipStream_t s) {
-    if (a.dtype == DT_BF16) few_rows<WF, DT_BF16>(a, s);
-    else few_rows<WF, DT_F16>(a, s);
+hipError_t few_format(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
+    if (a.dtype == DT_BF16) few_rows<WF, DT_BF16>(a, p, split, s);
+    else few_rows<WF, DT_F16>(a, p, split, s);
     return hipGetLastError();
 }
 
 // One translation unit a format (linear_few_*.hip).
-hipError_t launch_few_q4_0(const LinearArgs& a, hipStream_t s);
-hipError_t launch_few_affine4(const LinearArgs& a, hipStream_t s);
-hipError_t launch_few_affine8(const LinearArgs& a, hipStream_t s);
+hipError_t launch_few_q4_0(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s);
+hipError_t launch_few_affine4(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s);
+hipError_t launch_few_affine8(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s);
 
 }  // namespace q4

@@ -3,6 +3,8 @@
 
 namespace q4 {
 
-hipError_t launch_few_affine4(const LinearArgs& a, hipStream_t s) { return few_format<WF_AFFINE4>(a, s); }
+hipError_t launch_few_affine4(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
+    return few_format<WF_AFFINE4>(a, p, split, s);
+}
 
 }  // namespace q4

@@ -300,6 +300,15 @@ static void launch_shape(int epi, const TileArgs& a, unsigned grid, hipStream_t 
     else hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_LINEAR>), dim3(grid), dim3(256), 0, s, a);
 }
 
+hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s) {
+    const int64_t threads = a.epi.M * ((a.epi.N + 7) / 8);
+    if ((threads + 255) / 256 > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    if (nmat == 2) hipLaunchKernelGGL((k_tile_join<EPI_GATED>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_tile_join<EPI_LINEAR>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& args, hipStream_t s) {
     TileArgs a = args;
     a.parts = p.parts;
@@ -312,13 +321,7 @@ hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& args, h
     else if (p.nt == 4) launch_shape<4, 2>(epi, a, (unsigned)tiles, s);
     else if (p.mt == 4) launch_shape<2, 4>(epi, a, (unsigned)tiles, s);
     else launch_shape<2, 2>(epi, a, (unsigned)tiles, s);
-    if (p.parts > 1) {
-        const int64_t threads = a.epi.M * ((a.epi.N + 7) / 8);
-        if ((threads + 255) / 256 > 0x7FFFFFFF) return hipErrorInvalidValue;
-        const dim3 grid((unsigned)((threads + 255) / 256));
-        if (last == EPI_GATED) hipLaunchKernelGGL((k_tile_join<EPI_GATED>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((k_tile_join<EPI_LINEAR>), grid, dim3(256), 0, s, a);
-    }
+    if (p.parts > 1) return launch_tile_join(nmat, a, s);
     return hipGetLastError();
 }
 

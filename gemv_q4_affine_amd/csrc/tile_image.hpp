@@ -61,6 +61,8 @@ TilePlan plan_tiles(int nmat, int64_t M, int64_t N, int64_t K);
 int64_t partial_bytes(const TilePlan& p, int64_t M, int64_t w_panels);
 
 hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& a, hipStream_t s);
+// The parts of a split sum, joined, and the epilogue.
+hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s);
 // The weights as rows n (image of W) or as rows k (image of W^T, summed over
 // n); `mats` matrices side by side: panels alternate (rows n) or slices follow
 // each other (rows k).

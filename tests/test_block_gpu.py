@@ -209,6 +209,31 @@ def test_gated_backward(fmt, M, N, K):
         near(out["dup_bias"], dbu, F32, "dup_bias")
 
 
+# K of 32 steps and more (256 weights a step at 4 bits, 128 at 8) at 5 to 64 rows:
+# a sum in parts, the last of them shorter, with a K that ends inside a step; at 4
+# rows and at 31 steps one part.
+@pytest.mark.parametrize("fmt", R.FMTS)
+@pytest.mark.parametrize("M,N", [(4, 40), (5, 16), (16, 129), (17, 40), (33, 100), (64, 8)])
+@pytest.mark.parametrize("steps", [31, 32, 45])
+def test_long_sums_of_few_rows(fmt, M, N, steps):
+    gen = torch.Generator().manual_seed(M * 17 + N)
+    K = steps * (128 if fmt == "affine8" else 256) - 64
+    (gw, Wg), (uw, Wu) = weight(fmt, N, K, M + N), weight(fmt, N, K, M + N + 1)
+    for dt in (torch.bfloat16, torch.float16):
+        say(f"long sums {fmt} M={M} N={N} K={K} {dt}")
+        x, x64 = rand(gen, M, K, dtype=dt)
+        b, b64 = rand(gen, N, dtype=dt)
+        r, r64 = rand(gen, M, N, dtype=dt)
+        y, pre = Q.q4_linear(gw, x, bias=b, act=ACTS["gelu"], residual=r, save_pre=True)
+        y64, z64 = R.linear(x64, Wg, b64, "gelu", r64)
+        near(y, y64, bar(dt), "y")
+        near(pre, z64, bar(dt), "pre")
+        h, g, u = Q.q4_gated(gw, uw, x, gate_bias=b, save_pre=True)
+        for got, want, ops in zip((h, g, u), R.gated(x64, Wg, Wu, b64, None, "silu"), (4, 2, 2)):
+            near(got, want, bar(dt, ops), "gated")
+        assert torch.equal(Q.q4_gated(gw, uw, x, gate_bias=b), h), "not deterministic"
+
+
 @pytest.mark.parametrize("M", [3, 40, 300])
 def test_gradients_of_very_different_rows(M):
     """Rows of dz far above, far below and at the size of their dy, zero rows, and
