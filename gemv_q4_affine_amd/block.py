@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from .binding import Q4_FMT_AFFINE4, Q4_FMT_AFFINE8, Q4_FMT_Q4_0, _DT, _alloc_stream, _check, _dt, _stream, lib as _base_lib
+from .binding import Q4_BF16, Q4_FMT_AFFINE4, Q4_FMT_AFFINE8, Q4_FMT_Q4_0, _DT, _alloc_stream, _check, _dt, _stream, lib as _base_lib
 
 Q4_ACT_NONE, Q4_ACT_SILU, Q4_ACT_GELU, Q4_ACT_GELU_TANH, Q4_ACT_RELU = 0, 1, 2, 3, 4
 Q4_NORM_NONE, Q4_NORM_RMS, Q4_NORM_LAYER = 0, 1, 2
@@ -20,11 +20,11 @@ Q4_NORM_MAX_D = 32768
 
 _P, _I64, _INT, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
-    "q4_linear_workspace_size": (_I64, [_INT, _I64, _I64, _I64]),
+    "q4_linear_workspace_size": (_I64, [_INT, _INT, _I64, _I64, _I64]),
     "q4_linear": (_INT, [_INT, _P, _P, _P, _P, _INT, _P, _P, _INT, _P, _P, _I64, _I64, _I64, _P, _I64, _P]),
     "q4_linear_backward_workspace_size": (_I64, [_INT, _I64, _I64, _I64]),
     "q4_linear_backward": (_INT, [_INT, _P, _P, _P, _INT, _P, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P]),
-    "q4_gated_workspace_size": (_I64, [_INT, _I64, _I64, _I64]),
+    "q4_gated_workspace_size": (_I64, [_INT, _INT, _I64, _I64, _I64]),
     "q4_gated": (_INT, [_INT, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _P, _I64,
                         _P]),
     "q4_gated_backward_workspace_size": (_I64, [_INT, _I64, _I64, _I64]),
@@ -138,8 +138,8 @@ def _summed(t, name, shape, dtype, terms, like, stream):
 
 # ---- linear ---------------------------------------------------------------------
 
-def q4_linear_workspace_size(M, N, K, fmt=Q4_FMT_Q4_0) -> int:
-    return int(lib().q4_linear_workspace_size(fmt, M, N, K))
+def q4_linear_workspace_size(M, N, K, fmt=Q4_FMT_Q4_0, dtype=Q4_BF16) -> int:
+    return int(lib().q4_linear_workspace_size(fmt, dtype, M, N, K))
 
 
 def q4_linear(w, x, bias=None, act=Q4_ACT_NONE, residual=None, save_pre=False, y=None, pre=None, workspace="auto",
@@ -155,7 +155,7 @@ def q4_linear(w, x, bias=None, act=Q4_ACT_NONE, residual=None, save_pre=False, y
     if pre is None and save_pre:
         pre = _new((M, N), x.dtype, x, stream)
     _like(pre, "pre", (M, N), x.dtype)
-    ws, n = _workspace(workspace, q4_linear_workspace_size(M, N, K, fmt), x, stream)
+    ws, n = _workspace(workspace, q4_linear_workspace_size(M, N, K, fmt, _dt(x)), x, stream)
     _check("q4_linear", lib().q4_linear(fmt, *wp, _ptr(bias), act, _ptr(residual), _ptr(x), _dt(x), _ptr(y), _ptr(pre), M, N, K,
                                         _ptr(ws), n, _handle(stream, x)))
     return y if pre is None else (y, pre)
@@ -187,8 +187,8 @@ def q4_linear_backward(w, dy, act=Q4_ACT_NONE, pre=None, bias_grad=False, dx=Non
 
 # ---- gated ----------------------------------------------------------------------
 
-def q4_gated_workspace_size(M, N, K, fmt=Q4_FMT_Q4_0) -> int:
-    return int(lib().q4_gated_workspace_size(fmt, M, N, K))
+def q4_gated_workspace_size(M, N, K, fmt=Q4_FMT_Q4_0, dtype=Q4_BF16) -> int:
+    return int(lib().q4_gated_workspace_size(fmt, dtype, M, N, K))
 
 
 def _pair(gate, up):
@@ -214,7 +214,7 @@ def q4_gated(gate, up, x, act=Q4_ACT_SILU, gate_bias=None, up_bias=None, save_pr
         up_pre = _new((M, N), x.dtype, x, stream) if up_pre is None else up_pre
     _like(gate_pre, "gate_pre", (M, N), x.dtype)
     _like(up_pre, "up_pre", (M, N), x.dtype)
-    ws, n = _workspace(workspace, q4_gated_workspace_size(M, N, K, fmt), x, stream)
+    ws, n = _workspace(workspace, q4_gated_workspace_size(M, N, K, fmt, _dt(x)), x, stream)
     _check("q4_gated", lib().q4_gated(fmt, *gp, *upp, _ptr(gate_bias), _ptr(up_bias), act, _ptr(x), _dt(x), _ptr(h),
                                       _ptr(gate_pre), _ptr(up_pre), M, N, K, _ptr(ws), n, _handle(stream, x)))
     return h if gate_pre is None else (h, gate_pre, up_pre)

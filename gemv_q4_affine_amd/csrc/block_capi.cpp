@@ -61,9 +61,10 @@ int check_workspace(const void* ws, int64_t have, int64_t want) {
 int hip_status(hipError_t e) { return e == hipSuccess ? Q4_OK : Q4_ERR_HIP; }
 hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
-int64_t forward_bytes(int fmt, int nmat, int64_t M, int64_t N, int64_t K) {
+int64_t forward_bytes(int fmt, int nmat, int dtype, int64_t M, int64_t N, int64_t K) {
+    if (dtype != Q4_BF16 && dtype != Q4_F16) return 0;
     if (check_product(fmt, Q4_ACT_NONE, M, N, K) != Q4_OK || M == 0 || N == 0) return 0;
-    return q4::linear_workspace_bytes(format_wf(fmt), nmat, M, N, K);
+    return q4::linear_workspace_bytes(format_wf(fmt), nmat, dtype, M, N, K);
 }
 int64_t backward_bytes(int fmt, int nmat, int64_t M, int64_t N, int64_t K) {
     if (check_product(fmt, Q4_ACT_NONE, M, N, K) != Q4_OK || M == 0 || N == 0) return 0;
@@ -76,7 +77,9 @@ extern "C" {
 
 // ---- linear --------------------------------------------------------------------
 
-int64_t q4_linear_workspace_size(int fmt, int64_t M, int64_t N, int64_t K) { return forward_bytes(fmt, 1, M, N, K); }
+int64_t q4_linear_workspace_size(int fmt, int dtype, int64_t M, int64_t N, int64_t K) {
+    return forward_bytes(fmt, 1, dtype, M, N, K);
+}
 
 int q4_linear(int fmt, const uint8_t* w_q, const uint16_t* w_s, const uint16_t* w_b, const void* bias, int act,
               const void* residual, const void* x, int dtype, void* y, void* pre, int64_t M, int64_t N, int64_t K,
@@ -86,7 +89,7 @@ int q4_linear(int fmt, const uint8_t* w_q, const uint16_t* w_s, const uint16_t* 
     if (rc) return rc;
     if (M == 0 || N == 0) return Q4_OK;
     if ((rc = check_planes(fmt, w_q, w_s, w_b)) || (rc = need({x, y})) || (rc = optional({bias, residual, pre}))) return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, forward_bytes(fmt, 1, M, N, K)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, forward_bytes(fmt, 1, dtype, M, N, K)))) return rc;
     q4::LinearArgs a{};
     a.wf = format_wf(fmt);
     a.nmat = 1;
@@ -137,7 +140,9 @@ int q4_linear_backward(int fmt, const uint8_t* w_q, const uint16_t* w_s, const u
 
 // ---- gated ---------------------------------------------------------------------
 
-int64_t q4_gated_workspace_size(int fmt, int64_t M, int64_t N, int64_t K) { return forward_bytes(fmt, 2, M, N, K); }
+int64_t q4_gated_workspace_size(int fmt, int dtype, int64_t M, int64_t N, int64_t K) {
+    return forward_bytes(fmt, 2, dtype, M, N, K);
+}
 
 int q4_gated(int fmt, const uint8_t* gate_q, const uint16_t* gate_s, const uint16_t* gate_b, const uint8_t* up_q,
              const uint16_t* up_s, const uint16_t* up_b, const void* gate_bias, const void* up_bias, int act,
@@ -151,7 +156,7 @@ int q4_gated(int fmt, const uint8_t* gate_q, const uint16_t* gate_s, const uint1
     if ((rc = check_planes(fmt, gate_q, gate_s, gate_b)) || (rc = check_planes(fmt, up_q, up_s, up_b)) ||
         (rc = need({x, h})) || (rc = optional({gate_bias, up_bias, gate_pre, up_pre})))
         return rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, forward_bytes(fmt, 2, M, N, K)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, forward_bytes(fmt, 2, dtype, M, N, K)))) return rc;
     q4::LinearArgs a{};
     a.wf = format_wf(fmt);
     a.nmat = 2;

@@ -44,7 +44,7 @@ struct LinearGradArgs {
     float* dbias[2];
     int64_t M, N, K;
 };
-int64_t linear_workspace_bytes(int wf, int nmat, int64_t M, int64_t N, int64_t K);
+int64_t linear_workspace_bytes(int wf, int nmat, int dtype, int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s);
 int64_t linear_grad_workspace_bytes(int wf, int nmat, int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStream_t s);

@@ -34,8 +34,21 @@ Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M,
     l.total = l.sums_at + sums;
     return l;
 }
-Layout forward_layout(int nmat, int64_t M, int64_t N, int64_t K) {
+// rest: the sum runs over the weights rounded to binary16, then over what the
+// rounding left of them.
+Layout forward_layout(int nmat, bool rest, int64_t M, int64_t N, int64_t K) {
+    if (rest) K *= 2;
     return layout(plan_tiles(nmat, M, N, K), (N + 31) / 32 * nmat, image_slices(K), M, 0);
+}
+// A weight rounded to binary16 puts about as much error into a sum as the
+// rounding of a binary16 output does.  One such error (q4_linear with no
+// activation, or relu) leaves the output within 1.41 of its own rounding's; the
+// two of a gated product and a curved activation's slope made it 1.6 to 1.8
+// (affine4, 200 rows), so there the remainders are summed too, at twice the matrix
+// work (12288 x 4096, 512 rows, gated: 291 us against 148).  bfloat16 outputs are
+// eight times coarser.
+bool sums_rest(int nmat, int dtype, int act) {
+    return dtype == DT_F16 && (nmat == 2 || (act != ACT_NONE && act != ACT_RELU));
 }
 Layout backward_layout(int nmat, int64_t M, int64_t N, int64_t K) {
     const int64_t slices = image_slices(N) * nmat;
@@ -88,8 +101,13 @@ FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
 static int64_t few_rows_of(int64_t M) { return M <= kFewMaxM ? M : (M + 1) / 2; }
 static int64_t few_part_row(int nmat, int64_t N) { return (N + 31) / 32 * nmat * 32; }
 
-int64_t linear_workspace_bytes(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
-    if (M > kFewCallMaxM) return forward_layout(nmat, M, N, K).total;
+// Whatever the activation.
+int64_t linear_workspace_bytes(int wf, int nmat, int dtype, int64_t M, int64_t N, int64_t K) {
+    if (M > kFewCallMaxM) {
+        const int64_t one = forward_layout(nmat, false, M, N, K).total;
+        const int64_t two = dtype == DT_F16 ? forward_layout(nmat, true, M, N, K).total : 0;
+        return one > two ? one : two;
+    }
     const FewPlan p = plan_few(wf, nmat, few_rows_of(M), N, K);
     return p.parts > 1 ? p.parts * M * few_part_row(nmat, N) * 4 : 0;
 }
@@ -144,11 +162,12 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
         t.epi = epilogue_args(a);
         return launch_tile_join(a.nmat, t, s);
     }
-    const Layout l = forward_layout(a.nmat, a.M, a.N, a.K);
+    const bool rest = sums_rest(a.nmat, a.dtype, a.act);
+    const Layout l = forward_layout(a.nmat, rest, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, ws, s);
+    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, rest, ws, s);
     if (e == hipSuccess)
-        e = launch_pack_x(a.x, a.dtype, a.M, a.K, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at), s);
+        e = launch_pack_x(a.x, a.dtype, a.M, a.K, rest, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at), s);
     if (e != hipSuccess) return e;
     TileArgs t = tile_args(l, ws);
     t.epi = epilogue_args(a);
@@ -162,7 +181,7 @@ int64_t linear_grad_workspace_bytes(int, int nmat, int64_t M, int64_t N, int64_t
 hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStream_t s) {
     const Layout l = backward_layout(a.nmat, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, ws, s);
+    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, false, ws, s);
     if (e == hipSuccess)
         e = launch_pack_dz(a, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at),
                            reinterpret_cast<float*>(ws + l.sums_at), s);

@@ -65,10 +65,12 @@ hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& a, hipS
 hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s);
 // The weights as rows n (image of W) or as rows k (image of W^T, summed over
 // n); `mats` matrices side by side: panels alternate (rows n) or slices follow
-// each other (rows k).
-hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, uint8_t* img,
-                               hipStream_t s);
-hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, uint8_t* img, int8_t* xexp, hipStream_t s);
+// each other (rows k).  `rest` (rows n): after K terms the roundings' remainders;
+// the activations' image then holds its rows twice.
+hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, bool rest,
+                               uint8_t* img, hipStream_t s);
+hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool twice, uint8_t* img, int8_t* xexp,
+                         hipStream_t s);
 // dz of every projection: the image, the dz outputs and the column sums.
 int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N);
 hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s);

@@ -22,8 +22,10 @@
  *
  * dtype: Q4_BF16 or Q4_F16, the type of every activation tensor of the call.
  * Products are exact or binary16 x binary16 with binary32 accumulation
- * (weights dequantised to binary16, rounding <= 2^-11; x scaled per row by a
- * power of two so that the whole bfloat16 range fits); biases, activations,
+ * (weights dequantised to binary16, rounding <= 2^-11, absolute 2^-25 below
+ * 2^-14; x scaled per row by a power of two so that the whole bfloat16 range
+ * fits; for binary16 outputs of a gated product or under a curved activation the
+ * roundings' remainders are summed too); biases, activations,
  * products of projections, residuals and norms are computed in binary32 and
  * rounded once into the output.  The dequantised weights must fit binary16.
  */
@@ -59,10 +61,10 @@ extern "C" {
  *   pre      : device out, [M][N] of dtype: z (for the backward pass), or NULL
  *   K % 32 == 0 (Q4_0) or K % 64 == 0 (affine); N, K <= 2^25, M <= 2^30 (here
  *   and in the other products).
- *   workspace: q4_linear_workspace_size(fmt, M, N, K) bytes (0: may be NULL),
+ *   workspace: q4_linear_workspace_size(fmt, dtype, M, N, K) bytes (0: may be NULL),
  *              else Q4_ERR_WORKSPACE.  Calls sharing it must not overlap.
  */
-int64_t q4_linear_workspace_size(int fmt, int64_t M, int64_t N, int64_t K);
+int64_t q4_linear_workspace_size(int fmt, int dtype, int64_t M, int64_t N, int64_t K);
 int q4_linear(int fmt, const uint8_t* w_q, const uint16_t* w_s, const uint16_t* w_b, const void* bias, int act,
               const void* residual, const void* x, int dtype, void* y, void* pre, int64_t M, int64_t N, int64_t K,
               void* workspace, int64_t workspace_bytes, void* stream);
@@ -93,7 +95,7 @@ int q4_linear_backward(int fmt, const uint8_t* w_q, const uint16_t* w_s, const u
  *   gate_pre, up_pre : device out, [M][N] of dtype: g and u (for the backward
  *              pass), both or neither (else Q4_ERR_ARG)
  */
-int64_t q4_gated_workspace_size(int fmt, int64_t M, int64_t N, int64_t K);
+int64_t q4_gated_workspace_size(int fmt, int dtype, int64_t M, int64_t N, int64_t K);
 int q4_gated(int fmt, const uint8_t* gate_q, const uint16_t* gate_s, const uint16_t* gate_b, const uint8_t* up_q,
              const uint16_t* up_s, const uint16_t* up_b, const void* gate_bias, const void* up_bias, int act,
              const void* x, int dtype, void* h, void* gate_pre, void* up_pre, int64_t M, int64_t N, int64_t K,

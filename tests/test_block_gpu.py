@@ -209,6 +209,23 @@ def test_gated_backward(fmt, M, N, K):
         near(out["dup_bias"], dbu, F32, "dup_bias")
 
 
+@pytest.mark.parametrize("fmt", R.FMTS)
+@pytest.mark.parametrize("M,N,K", [(40, 96, 512), (66, 130, 192), (200, 256, 1024)])
+def test_binary16_outputs_are_those_of_exact_weights(fmt, M, N, K):
+    """What separates an output from the exact result is its own rounding: binary32
+    sums (F32) of weights exact to 2^-22."""
+    gen = torch.Generator().manual_seed(M + K)
+    (gw, Wg), (uw, Wu) = weight(fmt, N, K, 1, scale=0.05), weight(fmt, N, K, 2, scale=0.05)
+    x, x64 = rand(gen, M, K, dtype=torch.float16)
+    for act in ("silu", "gelu", "gelu_tanh", "relu"):
+        say(f"binary16 {fmt} M={M} N={N} K={K} {act}")
+        cases = [(Q.q4_gated(gw, uw, x, act=ACTS[act]), R.gated(x64, Wg, Wu, None, None, act)[0])]
+        if act != "relu":
+            cases.append((Q.q4_linear(gw, x, act=ACTS[act]), R.linear(x64, Wg, None, act, None)[0]))
+        for got, want in cases:
+            near(got, want, R.rel(want.half().double(), want) + F32, act)
+
+
 # K of 32 steps and more (256 weights a step at 4 bits, 128 at 8) at 5 to 64 rows:
 # a sum in parts, the last of them shorter, with a K that ends inside a step; at 4
 # rows and at 31 steps one part.
