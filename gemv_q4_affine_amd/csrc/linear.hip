@@ -81,7 +81,9 @@ TileArgs tile_args(const Layout& l, uint8_t* ws) {
 // Column tiles of a workgroup: one pair at q4_gated (12288 x 4096: 17.6 us at
 // one row against 18.1 with three pairs, 41.0 at 32 rows against 42.7 with two).
 // At q4_linear two where they fill the CUs (8192 x 4096, 32 rows: 15.6 against 19.2
-// with one; 512 x 12288 in 8 parts: 9.0, with one 7.8), three up to four rows.
+// with one; 512 x 12288 in 8 parts: 9.0, with one 7.8), three up to four rows, and
+// above where they make one round over the CUs of three (12288 x 4096, affine4, 32 rows:
+// 18.2 against 21.0 with two; Q4_0, 16 rows, 13.6 against 14.6; 8 bits the same).
 // Eight waves where the workgroups do not outnumber the CUs (4096 x 4096 gated, 32
 // rows: 16.4 against 20.8 with four).
 FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
@@ -89,7 +91,7 @@ FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = (N + 15) / 16, cus = current_cu_count(), pairs = (tiles + 1) / 2;
     const int64_t most = M > 4 && steps >= 32 ? steps / 8 : 1;
     FewPlan p{};
-    p.tiles = nmat == 2 || (most > 1 ? pairs * most < cus : tiles <= cus) ? 1 : tiles <= 2 * cus || M > 4 ? 2 : 3;
+    p.tiles = nmat == 2 || (most > 1 ? pairs * most < cus : tiles <= cus) ? 1 : tiles <= 2 * cus || (M > 4 && (most > 1 || tiles > 3 * cus)) ? 2 : 3;
     const int64_t groups = (tiles + p.tiles - 1) / p.tiles, room = 2 * cus / groups;
     const int64_t parts = room < 1 ? 1 : room < most ? room : most;
     p.per = (int)((steps + parts - 1) / parts);

@@ -40,7 +40,7 @@
 //
 // Bound: memory at 1 to 16 rows (each weight byte is read once).  Measured, Q4_0,
 // N = 12288, K = 4096: one row 9.5 us (28.3 MB; with no loads at all 4.4), 16
-// rows 14.6, 32 rows 21.5; the gated pair 17.6, 22.6 and 41.
+// rows 13.6, 32 rows 18.5; the gated pair 17.6, 22.6 and 41.
 #pragma once
 
 #include "block_common.hpp"
@@ -581,8 +581,8 @@ template <int WF, int XDT, int MT, bool DIAG>
 void few_tiles(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
     if (a.nmat == 2) few_waves<WF, XDT, MT, 1, true, DIAG>(a, p, split, s);
     else if (p.tiles == 1) few_waves<WF, XDT, MT, 1, false, DIAG>(a, p, split, s);
-    else if (p.tiles == 2 || !DIAG) few_waves<WF, XDT, MT, 2, false, DIAG>(a, p, split, s);
-    else few_waves<WF, XDT, MT, DIAG ? 3 : 2, false, DIAG>(a, p, split, s);
+    else if (p.tiles == 2) few_waves<WF, XDT, MT, 2, false, DIAG>(a, p, split, s);
+    else few_waves<WF, XDT, MT, 3, false, DIAG>(a, p, split, s);
 }
 template <int WF, int XDT>
 void few_rows(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
