@@ -582,7 +582,7 @@ void few_tiles(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hip
     if (a.nmat == 2) few_waves<WF, XDT, MT, 1, true, DIAG>(a, p, split, s);
     else if (p.tiles == 1) few_waves<WF, XDT, MT, 1, false, DIAG>(a, p, split, s);
     else if (p.tiles == 2) few_waves<WF, XDT, MT, 2, false, DIAG>(a, p, split, s);
-    else few_waves<WF, XDT, MT, 3, false, DIAG>(a, p, split, s);
+    else few_launch<WF, XDT, MT, 3, false, DIAG, 8>(a, p, split, s);      // one workgroup a CU, or up to four rows
 }
 template <int WF, int XDT>
 void few_rows(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {

@@ -262,13 +262,12 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
 
 // ---- gradients -----------------------------------------------------------------------
 //
-// Workgroup b takes the R rows b R .. of the M (R: about 1024 threads for every
-// CU of 256, grad_rows) and keeps, per column, its sums
-// for the weight and bias gradients and for the current gate row.  The sums go
+// Workgroup b takes the R rows b R .. of the M (grad_rows) and keeps, per column,
+// its sums for the weight and bias gradients and for the current gate row.  The sums go
 // to the workspace, [workgroup][pre_dw, pre_db, post_dw, post_db][D], and
 // k_norm_join adds them in workgroup order.  A gate row whose rows lie in one
 // workgroup is finished there; of the others a workgroup has at most two, its
-// first and its last, kept at [workgroup][2][D] for k_gate_join.
+// first and its last, kept at [workgroup][2][D] for k_norm_join.
 
 // Forms compiled apart, with every tensor there, for registers: the norms after
 // and before the block, and the one before it only (1000 x 1537, bfloat16: 8.9 us
