@@ -16,6 +16,7 @@
 // that are not a multiple of eight values, read element by element, took 21 us
 // for 1000 x 1537 against 7 with loads aligned to elements only.
 #include "tile_image.hpp"
+#include "wave_exchange.hpp"
 
 namespace q4 {
 
@@ -38,27 +39,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-constexpr int kMaxWaves = 16;
-
-// Sums of two values over the workgroup; `red` is this call site's own (one
-// barrier: it is written again only after a later call's barrier).
-__device__ __forceinline__ void row_sums(float& a, float& b, float (*red)[2]) {
+// Sums of two values over the workgroup (wave_sums: `red` and `turn`).
+__device__ __forceinline__ void row_sums(float& a, float& b, float (*red)[kMaxWaves][2], int& turn) {
     a = lanes_sum(a);
     b = lanes_sum(b);
-    if (blockDim.x > 64) {
-        const int lane = threadIdx.x & 63;
-        if (lane == 0) {
-            red[threadIdx.x >> 6][0] = a;
-            red[threadIdx.x >> 6][1] = b;
-        }
-        __syncthreads();
-        const int waves = (int)(blockDim.x >> 6);
-        a = b = 0.0f;
-        for (int w = 0; w < waves; w++) {
-            a += red[w][0];
-            b += red[w][1];
-        }
-    }
+    if (blockDim.x > 64)
+        wave_sums(a, b, (int)(threadIdx.x >> 6), (int)(blockDim.x >> 6), (threadIdx.x & 63) == 0, red, turn,
+                  []() __attribute__((always_inline)) { __syncthreads(); });
 }
 
 // Element o of a tensor: o is the same in all lanes, so that an access is a
@@ -156,7 +143,8 @@ __device__ __forceinline__ Raw8<DT> vector8(const void* p, uint32_t i, int left,
 // requested before this row's sums.
 template <int DT, int RT, int V, bool VEC>
 __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormArgs a) {
-    __shared__ float red[4][kMaxWaves][2];
+    __shared__ float red[2][kMaxWaves][2];
+    int turn = 0;
     const int tid = threadIdx.x, T = blockDim.x;
     const int64_t D = a.D;
     const float inv = 1.0f / (float)D;
@@ -182,8 +170,7 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
         }
     };
     // mean and 1 / sqrt(variance + eps) of x, by the norm's kind
-    auto stats = [&](const float (&x)[V][8], int kind, float& mean, float& rstd, float (*red0)[2], float (*red1)[2])
-        __attribute__((always_inline)) {
+    auto stats = [&](const float (&x)[V][8], int kind, float& mean, float& rstd) __attribute__((always_inline)) {
         float s = 0.0f, unused = 0.0f;
         mean = 0.0f;
         rstd = 1.0f;
@@ -193,7 +180,7 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
             for (int v = 0; v < V; v++)
 #pragma unroll
                 for (int e = 0; e < 8; e++) s += x[v][e];          // zeros past the row's end
-            row_sums(s, unused, red0);
+            row_sums(s, unused, red, turn);
             mean = s * inv;
             s = 0.0f;
         }
@@ -204,7 +191,7 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
                 const float d = inside<VEC>(e, left[v]) ? x[v][e] - mean : 0.0f;
                 s = fmaf(d, d, s);
             }
-        row_sums(s, unused, red1);
+        row_sums(s, unused, red, turn);
         rstd = 1.0f / sqrtf(fmaf(s, inv, a.eps));
     };
     int64_t m = blockIdx.x;
@@ -229,7 +216,7 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
 #pragma unroll
             for (int v = 0; v < V; v++)
                 gate[v] = vector8<DT, VEC>(a.gate ? from<DT>(a.gate, gr * D) : nullptr, (uint32_t)(v * T + tid) * 8, left[v], true);
-            stats(y, a.post, m0, i0, red[0], red[1]);
+            stats(y, a.post, m0, i0);
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 float w[8], b[8], g[8];
@@ -244,7 +231,7 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
                 put8<RT, VEC>(from<RT>(a.r_out, o), (uint32_t)(v * T + tid) * 8, left[v], r[v]);
             }
         }
-        stats(r, a.pre, m1, i1, red[2], red[3]);
+        stats(r, a.pre, m1, i1);
         if (a.n) {
 #pragma unroll
             for (int v = 0; v < V; v++) {
@@ -278,6 +265,7 @@ template <int DT, int RT, int V, bool VEC, bool BIAS, int FORM>
 __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int64_t R, float* __restrict__ sums,
                                                          float* __restrict__ pieces) {
     __shared__ float red[2][kMaxWaves][2];
+    int turn = 0;
     const int tid = threadIdx.x, T = blockDim.x;
     const bool has_dn = FORM || a.dn, has_dr = FORM || a.dr_out, has_y = FORM || a.y;
     const bool has_post = FORM == FORM_BOTH || (FORM == FORM_ANY && a.post != NORM_NONE);
@@ -356,7 +344,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int64_
                 }
             }
             if (m + 1 < r1) request(m + 1);
-            row_sums(c1, c2, red[0]);
+            row_sums(c1, c2, red, turn);
             c1 = a.pre == NORM_LAYER ? c1 * inv : 0.0f;
             c2 *= inv;
 #pragma unroll
@@ -397,7 +385,7 @@ __global__ __launch_bounds__(1024) void k_norm_grad(const NormGradArgs a, int64_
             }
         }
         if (has_post) {
-            row_sums(c1, c2, red[1]);
+            row_sums(c1, c2, red, turn);
             c1 = a.post == NORM_LAYER ? c1 * inv : 0.0f;
             c2 *= inv;
 #pragma unroll
