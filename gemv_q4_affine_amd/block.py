@@ -326,7 +326,8 @@ def block_norm_backward(r_out, y, stats, dn=None, dr_out=None, pre_norm=Q4_NORM_
     if y is not None:
         out["dy"] = _new((M, D), dt, r_out, stream)
     if gate is not None:
-        out["dgate"] = _new(_like(gate, "gate", (gate.shape[0], D), dt).shape, dt, r_out, stream)
+        _like(gate, "gate", (gate.shape[0], D), dt)
+        out["dgate"] = _summed(None, "dgate", gate.shape, dt, M, r_out, stream)
     for name, t in (("pre_dw", pre_weight), ("pre_db", pre_bias), ("post_dw", post_weight), ("post_db", post_bias)):
         if t is not None:
             out[name] = _summed(None, name, (D,), torch.float32, M, r_out, stream)

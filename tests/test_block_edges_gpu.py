@@ -1,0 +1,32 @@
+"""The feed-forward operators at the edges of their arguments, on the GPU."""
+import pytest
+import torch
+
+import gemv_q4_affine_amd as Q
+
+pytestmark = pytest.mark.gpu
+
+
+def used_memory(*shape, dtype):
+    """Leaves memory of this size, full of NaN, for the next allocation of it."""
+    t = torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+    torch.cuda.synchronize()
+    del t
+
+
+@pytest.mark.parametrize("stream", [False, True])
+def test_norm_gradients_of_no_rows(stream):
+    """Sums over no rows are zeros: the gate's gradient among them."""
+    D, groups, dt = 96, 5, torch.bfloat16
+    none = torch.zeros(0, D, dtype=dt, device="cuda")
+    w, gate = torch.ones(D, dtype=dt, device="cuda"), torch.ones(groups, D, dtype=dt, device="cuda")
+    s = torch.cuda.Stream() if stream else None
+    with torch.cuda.stream(s):
+        used_memory(groups, D, dtype=dt)
+        used_memory(D, dtype=torch.float32)
+    out = Q.block_norm_backward(none, none, torch.zeros(0, 4, device="cuda"), none, none, pre_weight=w, pre_bias=w,
+                                post_norm=Q.Q4_NORM_LAYER, post_weight=w, post_bias=w, gate=gate, stream=s)
+    torch.cuda.synchronize()
+    assert out["dr"].shape == out["dy"].shape == (0, D) and out["dgate"].shape == (groups, D)
+    for name in ("dgate", "pre_dw", "pre_db", "post_dw", "post_db"):
+        assert (out[name] == 0).all(), name
