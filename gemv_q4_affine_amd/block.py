@@ -174,7 +174,7 @@ def q4_linear_backward(w, dy, act=Q4_ACT_NONE, pre=None, bias_grad=False, dx=Non
     _like(dy, "dy", (M, N), dy.dtype)
     _like(pre, "pre", (M, N), dy.dtype)
     out = {"dx": _summed(dx, "dx", (M, K), dy.dtype, N, dy, stream)}
-    if act != Q4_ACT_NONE:
+    if act != Q4_ACT_NONE or dz is not None:              # the library refuses a dz that would be dy
         out["dz"] = _out(dz, "dz", (M, N), dy.dtype, dy, stream)
     if bias_grad or dbias is not None:
         out["dbias"] = _summed(dbias, "dbias", (N,), torch.float32, M, dy, stream)

@@ -30,3 +30,16 @@ def test_norm_gradients_of_no_rows(stream):
     assert out["dr"].shape == out["dy"].shape == (0, D) and out["dgate"].shape == (groups, D)
     for name in ("dgate", "pre_dw", "pre_db", "post_dw", "post_db"):
         assert (out[name] == 0).all(), name
+
+
+def test_a_dz_that_would_be_dy_is_refused():
+    """Without an activation dz is dy: the C ABI refuses a dz output, and so does the
+    binding, which must not leave the caller's tensor unwritten."""
+    w = Q.q4_quantize(torch.randn(64, 64, device="cuda"))
+    dy = torch.ones(3, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(Q.Q4Error):
+        Q.q4_linear_backward(w, dy, dz=torch.empty_like(dy))
+    assert set(Q.q4_linear_backward(w, dy)) == {"dx"}
+    dz = torch.zeros_like(dy)
+    out = Q.q4_linear_backward(w, dy, act=Q.Q4_ACT_RELU, pre=dy, dz=dz)
+    assert out["dz"] is dz and torch.equal(dz, dy)
