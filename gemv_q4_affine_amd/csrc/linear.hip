@@ -160,6 +160,7 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
         TileArgs t{};
         t.part = part;
         t.parts = p.parts;
+        t.unit = few_unit(a.wf, a.dtype);
         t.w_panels = (a.N + 31) / 32 * a.nmat;
         t.epi = epilogue_args(a);
         return launch_tile_join(a.nmat, t, s);

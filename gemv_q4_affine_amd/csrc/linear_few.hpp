@@ -9,7 +9,10 @@
 //   affine  y += s sum x q + b sum x                    per group of 64
 // with bfloat16 x: 128 + q (4 bits) or q (8 bits) is exact in bfloat16, and the
 // subtracted multiple of sum x is the MFMA's accumulator input, itself one MFMA
-// of x against a constant that serves every column.  With binary16 x the codes
+// of x against a constant that serves every column.  All of these operands carry
+// a factor 2^-14 (8 bits: 2^-15), taken off the joined sum again: a block's
+// sums then stay in binary32's range for every x (64 terms of 255 x 2^-15, 143 x
+// 2^-14 or 128 x 2^-14), and the products' bits are the same.  With binary16 x the codes
 // are q - 8 and q themselves.  Products are exact, sums binary32: the result
 // differs from the exact one by binary32 summation and the output's rounding.
 //
@@ -85,11 +88,16 @@ __device__ __forceinline__ floatx4_t mfma16(const u32x4_t& x, const u32x4_t& w, 
                                                       0, 0);
 }
 
+// The factor of the codes and offsets beside bfloat16 x is 2^-this (see above).
+template <int WF, int XDT> constexpr int kDown = XDT != DT_BF16 ? 0 : WF == WF_AFFINE8 ? 15 : 14;
+// A constant of them, twice: the bfloat16 bits of c 2^-this (exponents subtract).
+template <int WF> constexpr uint32_t lowered(uint32_t bits) { return (bits - (kDown<WF, DT_BF16> << 7)) * 0x10001u; }
+
 // Eight codes of a dword, in the pair order (byte 0, byte 2), (1, 3) of the low
-// nibbles, then of the high ones: bfloat16 128 + q, binary16 q - SUB.
+// nibbles, then of the high ones: bfloat16 (128 + q) 2^-14, binary16 q - SUB.
 template <int XDT, int SUB>
 __device__ __forceinline__ u32x4_t nibbles(uint32_t w, uint32_t mask) {
-    const uint32_t base = XDT == DT_BF16 ? 0x43004300u : 0x64006400u;
+    const uint32_t base = XDT == DT_BF16 ? lowered<WF_Q4_0>(0x4300u) : 0x64006400u;
     u32x4_t r;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
@@ -105,7 +113,9 @@ __device__ __forceinline__ u32x4_t nibbles(uint32_t w, uint32_t mask) {
     }
     return r;
 }
-// Eight 8-bit codes, exact in either type, in order.
+// Eight 8-bit codes, exact in either type, in order (bfloat16: q 2^-15; the
+// subtraction from the exponent saturates, so that a zero stays one).
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 template <int XDT>
 __device__ __forceinline__ u32x4_t bytes8(uint32_t lo, uint32_t hi) {
     u32x4_t r;
@@ -113,7 +123,10 @@ __device__ __forceinline__ u32x4_t bytes8(uint32_t lo, uint32_t hi) {
     for (int e = 0; e < 4; e++) {
         const uint32_t w = e < 2 ? lo : hi;
         const f32x2_t f = {(float)((w >> (16 * (e & 1))) & 0xFFu), (float)((w >> (16 * (e & 1) + 8)) & 0xFFu)};
-        if constexpr (XDT == DT_BF16) r[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2_t));
+        if constexpr (XDT == DT_BF16)
+            r[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(
+                                                    __builtin_bit_cast(u16x2_t, __builtin_convertvector(f, bf16x2_t)),
+                                                    __builtin_bit_cast(u16x2_t, (kDown<WF_AFFINE8, DT_BF16> << 7) * 0x10001u)));
         else r[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, half2_t));
     }
     return r;
@@ -122,7 +135,8 @@ __device__ __forceinline__ u32x4_t bytes8(uint32_t lo, uint32_t hi) {
 }  // namespace few
 
 // A sum split over workgroups: part blockIdx.y takes `per` steps and leaves its
-// sums in rows of `np` values (the order of k_tile_join), unrounded.
+// sums in rows of `np` values (the order of k_tile_join), unrounded and with
+// their factor 2^-kDown.
 struct FewSplit {
     float* part;          // null: one part, the epilogue here
     int64_t rows, np;     // rows of a part (of the whole call)
@@ -287,7 +301,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a
             for (int r = 0; r < 4; r++) x[0][r] = *reinterpret_cast<const u32x4_t*>(p + r * 16);
             // Q4_0: codes less 8; affine: the sums of x for the group's bias too
             constexpr bool kOffset = XDT == DT_BF16;
-            const uint32_t one = WF == WF_Q4_0 ? 0xC308C308u : kOffset ? 0xC300C300u : 0x3C003C00u;
+            const uint32_t one = WF == WF_Q4_0 ? lowered<WF>(0xC308u) : kOffset ? lowered<WF>(0xC300u) : 0x3C003C00u;
             floatx4_t cs = zero;
             if (kOffset || WF == WF_AFFINE4) {
 #pragma unroll
@@ -321,7 +335,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a
                 floatx4_t c0[MT];
 #pragma unroll
                 for (int i = 0; i < MT; i++)
-                    c0[i] = XDT == DT_BF16 ? mfma16<XDT>(x[i][t], splat(0xC308C308u), zero) : zero;      // -136 sum x
+                    c0[i] = XDT == DT_BF16 ? mfma16<XDT>(x[i][t], splat(lowered<WF>(0xC308u)), zero) : zero;      // -136 sum x
 #pragma unroll
                 for (int n = 0; n < NT; n++) {
                     const u32x4_t c = nibbles<XDT, 8>(w[n].q[0][t], mask);
@@ -341,7 +355,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a
             }
             // 4 bits, bfloat16: the codes are 128 + q, so the sums of x enter as -128 sum x
             constexpr bool kOffset = WF == WF_AFFINE4 && XDT == DT_BF16;
-            const uint32_t one = kOffset ? 0xC300C300u : XDT == DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
+            const uint32_t one = kOffset ? lowered<WF>(0xC300u) : XDT == DT_BF16 ? lowered<WF>(0x3F80u) : 0x3C003C00u;
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 floatx4_t cs[MT];
@@ -529,6 +543,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a
             return v;
         };
         const int64_t at = (int64_t)m * N + n;
+        constexpr float kUp = (float)(1 << kDown<WF, XDT>);
         float z = sum(GATED ? 2 * p : p);
         if (split.part) {
             float* row = split.part + ((int64_t)blockIdx.y * split.rows + m) * split.np;
@@ -536,13 +551,14 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a
             if constexpr (GATED) row[(n >> 5) * 64 + 32 + (n & 31)] = sum(2 * p + 1);
             continue;
         }
+        z *= kUp;
         if (a.bias[0]) z += load_elem(a.bias[0], XDT, n);
         if (a.pre[0]) store_elem(a.pre[0], XDT, at, z);
         float zs[1] = {z}, none[1];
         activate_all<false>(a.act, zs, zs, none);
         float y = zs[0];
         if constexpr (GATED) {
-            float u = sum(2 * p + 1);
+            float u = sum(2 * p + 1) * kUp;
             if (a.bias[1]) u += load_elem(a.bias[1], XDT, n);
             if (a.pre[1]) store_elem(a.pre[1], XDT, at, u);
             y *= u;
@@ -562,6 +578,10 @@ struct FewPlan {
     int tiles, waves, parts, per;
 };
 FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K);
+// What takes the factor off the sums of a split again.
+inline float few_unit(int wf, int dtype) {
+    return dtype != DT_BF16 ? 1.0f : (float)(1 << (wf == WF_AFFINE8 ? few::kDown<WF_AFFINE8, DT_BF16> : few::kDown<WF_Q4_0, DT_BF16>));
+}
 
 template <int WF, int XDT, int MT, int P, bool GATED, bool DIAG, int WAVES>
 void few_launch(const LinearArgs& a, const FewPlan& plan, FewSplit split, hipStream_t s) {

@@ -181,7 +181,8 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     for (int j = 0; j < MT; j++) {
         const int64_t m0 = (pm0 + wm * MT + j) * 32;
         const int64_t mine = m0 + (lane & 31);
-        const float back = mine < M ? ldexpf(1.0f, -(int)a.xexp[mine]) : 0.0f;
+        // (parts of a sum are joined first: alone they may leave the range)
+        const float back = EPI == EPI_PARTIAL ? 1.0f : mine < M ? ldexpf(1.0f, -(int)a.xexp[mine]) : 0.0f;
         // lane: row lane & 31 of the panel, columns 8 (e / 4) + 4 (lane >> 5) + e % 4
 #pragma unroll
         for (int i = 0; i < NT; i++)
@@ -229,8 +230,8 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     }
 }
 
-// The parts of a split sum joined in order, then the epilogue: one thread for
-// eight columns of a row.
+// The parts of a split sum joined in order and scaled, then the epilogue: one
+// thread for eight columns of a row.
 template <int EPI>
 __global__ __launch_bounds__(256) void k_tile_join(const TileArgs a) {
     const int64_t chunks = (a.epi.N + 7) / 8;
@@ -251,6 +252,12 @@ __global__ __launch_bounds__(256) void k_tile_join(const TileArgs a) {
         };
         add(row, z);
         if constexpr (EPI == EPI_GATED) add(row + 32, z2);
+    }
+    const float back = a.xexp ? ldexpf(1.0f, -(int)a.xexp[m]) : a.unit;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        z[e] *= back;
+        z2[e] *= back;
     }
     if (a.epi.N % 8 == 0) epilogue8<EPI, true>(a.epi, m, n, z, z2);
     else epilogue8<EPI, false>(a.epi, m, n, z, z2);

@@ -44,11 +44,12 @@ struct EpilogueArgs {
 struct TileArgs {
     const uint8_t* wimg;
     const uint8_t* ximg;
-    const int8_t* xexp;        // row m of the x image holds x * 2^xexp[m]
+    const int8_t* xexp;        // row m of the x image holds x * 2^xexp[m] (null: see unit)
     int64_t slices;            // of both images
     int64_t w_panels, x_panels;
     int parts;                 // parts of the slices (EPI_PARTIAL), else 1
-    float* part;               // [parts][M][N'] sums, N' = w_panels * 32
+    float* part;               // [parts][M][N'] sums as they were added up, N' = w_panels * 32
+    float unit;                // of them where there is no xexp
     EpilogueArgs epi;
 };
 

@@ -1,0 +1,71 @@
+"""The products over the whole range of their operands' types, on both sides of the
+few-row kernels (64 rows): against binary64, row by row.  Tolerances as in
+test_block_gpu (`bar`), and bfloat16's absolute spacing below 2^-126 (2^-133).
+"""
+import pytest
+import torch
+
+import block_reference as R
+import gemv_q4_affine_amd as Q
+import test_block_gpu as G
+
+pytestmark = pytest.mark.gpu
+
+ROWS = [1, 3, 4, 5, 16, 17, 33, 64, 65, 200]
+
+
+def rows_near(got, want, dtype, what):
+    got, want = got.double().cpu(), want.double().cpu()
+    for m in range(got.shape[0]):
+        e, n = (got[m] - want[m]).norm().item(), want[m].norm().item()
+        assert e <= G.bar(dtype) * n + 2.0 ** -132 * want.shape[1] ** 0.5, (what, m, e / n)
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("fmt", R.FMTS)
+@pytest.mark.parametrize("K", [64, 512, 4096])
+def test_largest_and_smallest_x(fmt, M, K):
+    """bfloat16 x up to the type's largest value, in either sign or all of one, and
+    down to its normal range's end; outputs are in range.  Where x is all of one sign,
+    W's codes are what they are: sums of whole blocks at the top of the range."""
+    gen = torch.Generator().manual_seed(M * 7 + K)
+    N = 48
+    (w, W), (u, U) = G.weight(fmt, N, K, M, scale=1e-3), G.weight(fmt, N, K, M + 1, scale=1e-3)
+    top = torch.finfo(torch.bfloat16).max
+    x = torch.rand(M, K, generator=gen) * torch.tensor([-1.0, 1.0])[torch.randint(0, 2, (M, K), generator=gen)]
+    kind = torch.arange(M) % 5
+    x[kind == 1] = x[kind == 1].abs()
+    x[kind == 2] = 1.0
+    size = torch.tensor([top, top, top, 2.0 ** -110, 2.0 ** -120])[(kind + M) % 5]
+    # a row whose exact sums leave the type takes 1/4, 1/16 .. of the size
+    for m in range(M):
+        while ((x[m].double() * size[m].double()) @ torch.stack([W, U]).transpose(1, 2)).abs().max() > 0.9 * top:
+            size[m] /= 4
+    x = (x.double() * size[:, None].double()).bfloat16()
+    assert torch.isfinite(x).all()
+    y, pre = Q.q4_linear(w, x.cuda(), save_pre=True)
+    rows_near(y, x.double() @ W.T, torch.bfloat16, "y")
+    assert torch.equal(pre, y)
+    _, g, up = Q.q4_gated(w, u, x.cuda(), act=Q.Q4_ACT_RELU, save_pre=True)
+    rows_near(g, x.double() @ W.T, torch.bfloat16, "gate")
+    rows_near(up, x.double() @ U.T, torch.bfloat16, "up")
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("fmt", R.FMTS)
+def test_largest_codes(fmt, M):
+    """Every code the largest (and the smallest) and every x the largest: the block
+    sums are as large as they get."""
+    N, K = 32, 256
+    top = torch.finfo(torch.bfloat16).max
+    for code in (0, 255):
+        q = torch.full((N, K // (1 if fmt == "affine8" else 2)), code, dtype=torch.uint8, device="cuda")
+        most = 255 if fmt == "affine8" else 15
+        if fmt == "q4_0":
+            d = torch.full((N, K // 32), 2.0 ** -13).half()
+            w, value = (q.view(N, K // 32, 16), d.view(torch.int16).cuda()), 2.0 ** -13 * (code % 16 - 8)
+        else:
+            s, b = torch.full((N, K // 64), 2.0 ** -18).bfloat16(), torch.full((N, K // 64), -(2.0 ** -12)).bfloat16()
+            w, value = (q, s.view(torch.int16).cuda(), b.view(torch.int16).cuda()), 2.0 ** -18 * min(code, most) - 2.0 ** -12
+        x = torch.full((M, K), top).bfloat16()
+        rows_near(Q.q4_linear(w, x.cuda()), torch.full((M, N), top * value * K, dtype=torch.float64), torch.bfloat16, code)
