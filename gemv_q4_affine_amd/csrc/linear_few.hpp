@@ -143,6 +143,37 @@ struct FewSplit {
     int per, x_shift;
 };
 
+// Output n of a row x whose sum z over k0 <= k < k1 came out as NaN.  The sums
+// above hold an infinite x with either sign (x (128 + q) - 136 x, s x q + b x), so
+// that one infinity already gives a NaN; the infinite terms w x themselves
+// decide what the sum is.  Without any z stays.  Reached by spoilt rows only.
+template <int WF>
+__device__ __forceinline__ float spoilt_sum(const QuantW& w, const uint16_t* x, int xdt, int64_t n, int64_t K, int k0, int k1,
+                                            float z) {
+    const uint32_t top = xdt == DT_BF16 ? 0x7F80u : 0x7C00u;
+    float t = 0.0f;
+    bool any = false;
+#pragma unroll 1
+    for (int k = k0; k < k1 && t == t; k += 8) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + k);
+#pragma unroll 1
+        for (int e = 0; e < 8; e++) {
+            const uint32_t h = (v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+            if ((h & top) != top) continue;
+            const int64_t at = n * K + k + e;
+            float q;
+            if constexpr (WF == WF_AFFINE8) q = (float)w.q[at];
+            else if constexpr (WF == WF_AFFINE4) q = (float)((w.q[at / 2] >> (4 * (at & 1))) & 15u);
+            else q = (float)((w.q[at / 32 * 16 + (at & 15)] >> (at & 16 ? 4 : 0)) & 15u) - 8.0f;
+            const float wk = WF == WF_Q4_0 ? q * f16_to_f32(w.s[at / 32])
+                                           : __builtin_fmaf(q, bf16_to_f32(w.s[at / 64]), bf16_to_f32(w.b[at / 64]));
+            t = __builtin_fmaf(wk, xdt == DT_BF16 ? bf16_to_f32(h) : f16_to_f32(h), t);
+            any = true;
+        }
+    }
+    return any ? t : z;
+}
+
 // Waves and LDS of a variant.  What is in flight on a CU is a step a wave: up to
 // four rows a workgroup has eight waves, above them four, so that two workgroups
 // with their x share a CU, or eight where there is but one workgroup a CU.
@@ -540,6 +571,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void k_linear_few(const LinearArgs a
         auto sum = [&](int t) __attribute__((always_inline)) {
             float v = red[t * kTile + m * 16 + col];
             for (int w = 1; w < waves; w++) v += red[(w * NT + t) * kTile + m * 16 + col];
+            if (v != v) {
+                const int k0 = s0 * kStep, k1 = k0 + steps * kStep;
+                v = spoilt_sum<WF>(a.w[GATED ? t & 1 : 0], static_cast<const uint16_t*>(a.x) + (int64_t)m * K, XDT, n, K, k0,
+                                   k1 < K ? k1 : K, v);
+            }
             return v;
         };
         const int64_t at = (int64_t)m * N + n;

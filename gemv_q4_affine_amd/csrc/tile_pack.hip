@@ -232,8 +232,12 @@ hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int
 // in two halves.  Measured: 2048 x 4096 10 us, 2048 x 12288 19 us (5.3 TB/s).
 constexpr int kPackThreads = 1024;
 
+constexpr float kLargest = 3.4028234663852886e38f;
+
+// Of a row's largest |value| (NaNs left out).
 __device__ __forceinline__ int row_exponent(float mx) {
-    if (!(mx > 0.0f) || mx > 3.4028234663852886e38f) return 0;          // zero, infinite or NaN
+    if (!(mx > 0.0f)) return 0;
+    if (mx > kLargest) return -113;        // an infinity: no finite value beside it becomes one
     const int e = 14 - (__builtin_amdgcn_frexp_expf(mx) - 1);
     return e < -113 ? -113 : e > 127 ? 127 : e;
 }
@@ -284,7 +288,12 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_rows(const void* __restri
             for (int i = 0; i < 8; i++) v[i] *= scale;
             const u32x4_t p = pack8(DT_F16, v);
             *reinterpret_cast<u32x4_t*>(piece(img, m, slices, c)) = p;
-            if (twice) *reinterpret_cast<u32x4_t*>(piece(img, m, slices, c + chunks)) = p;
+            if (twice) {
+                // an infinity counts in the first half only: a remainder may be zero
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = fabsf(v[i]) <= kLargest ? v[i] : 0.0f;
+                *reinterpret_cast<u32x4_t*>(piece(img, m, slices, c + chunks)) = pack8(DT_F16, v);
+            }
         }
         if (threadIdx.x < ROWS) xexp[m] = (int8_t)e;
     }
@@ -400,8 +409,8 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_dz(const LinearGradArgs a
         if (exact || again) break;
         __syncthreads();                                     // `red` is read no more
         mx = rows_max<ROWS>(mx, red);
-        const int at = mx > 0.0f && mx <= 3.4028234663852886e38f ? __builtin_amdgcn_frexp_expf(mx) - 1 + e : 0;
-        const bool miss = at < -2 || at >= 15;
+        const int at = mx > 0.0f && mx <= kLargest ? __builtin_amdgcn_frexp_expf(mx) - 1 + e : 0;
+        const bool miss = at < -2 || at >= 15 || (mx > kLargest && e > -113);
         if (miss) e = row_exponent(mx);
         if (!__syncthreads_or(miss)) break;
     }

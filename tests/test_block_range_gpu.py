@@ -69,3 +69,81 @@ def test_largest_codes(fmt, M):
             w, value = (q, s.view(torch.int16).cuda(), b.view(torch.int16).cuda()), 2.0 ** -18 * min(code, most) - 2.0 ** -12
         x = torch.full((M, K), top).bfloat16()
         rows_near(Q.q4_linear(w, x.cuda()), torch.full((M, N), top * value * K, dtype=torch.float64), torch.bfloat16, code)
+
+
+def same_kind(got, want, dtype, what):
+    """Infinities and NaN where binary64 has them; the rest near, row by row."""
+    got, want = got.double().cpu(), want.double().cpu()
+    assert torch.equal(got.isnan(), want.isnan()), (what, (got.isnan() != want.isnan()).nonzero()[:5])
+    inf = want.isinf()
+    assert torch.equal(got[inf], want[inf]), what
+    ok = torch.isfinite(want)
+    assert torch.isfinite(got[ok]).all(), what
+    rows_near(torch.where(ok, got, 0), torch.where(ok, want, 0), dtype, what)
+
+
+def times(x, W):
+    """x . W^T by its definition: a zero weight and an infinity make a NaN, a zero x and a
+    finite weight do not."""
+    return torch.stack([(row * W).sum(1) for row in x])
+
+
+def spoil(x, largest):
+    """One infinity of either sign, beside large values; two of the same and of opposite
+    signs; a NaN; in rows of their own."""
+    for m in range(x.shape[0]):
+        k = (37 * m + 11) % x.shape[1]
+        j = (k + 20) % x.shape[1]
+        kind = m % 7
+        if kind in (0, 2):
+            x[m, k] = float("inf" if kind == 0 else "-inf")
+            x[m, (k + 1) % x.shape[1]] = -largest
+        elif kind in (1, 3):
+            x[m, k] = float("inf")
+            x[m, j] = float("inf" if kind == 1 else "-inf")
+        elif kind == 4:
+            x[m, k] = float("nan")
+    return x
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 16, 20, 33, 64, 65, 200])
+@pytest.mark.parametrize("fmt", R.FMTS)
+@pytest.mark.parametrize("K", [192, 8192])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_infinities_in_x(fmt, M, K, dt):
+    """A row with an infinity is what its infinite terms make it, and no other row is."""
+    gen = torch.Generator().manual_seed(M + K)
+    N, dt = 40, G.DT[dt]
+    (w, W), (u, U) = G.weight(fmt, N, K, M), G.weight(fmt, N, K, M + 1)
+    x = spoil(torch.randn(M, K, generator=gen), 3e38 if dt == torch.bfloat16 else 6e4).to(dt)
+    g64, u64 = times(x.double(), W), times(x.double(), U)
+    y, pre = Q.q4_linear(w, x.cuda(), act=Q.Q4_ACT_GELU, save_pre=True)
+    same_kind(pre, g64, dt, "pre")
+    same_kind(Q.q4_linear(w, x.cuda()), g64, dt, "y")
+    _, g, up = Q.q4_gated(w, u, x.cuda(), save_pre=True)
+    same_kind(g, g64, dt, "gate")
+    same_kind(up, u64, dt, "up")
+
+
+@pytest.mark.parametrize("M", [1, 9, 64, 200])
+@pytest.mark.parametrize("fmt", R.FMTS)
+def test_infinities_in_gradients(fmt, M):
+    gen = torch.Generator().manual_seed(M)
+    N, K = 40, 128
+    (w, W), (u, U) = G.weight(fmt, N, K, M), G.weight(fmt, N, K, M + 1)
+    dy = spoil(torch.randn(M, N, generator=gen), 3e38).bfloat16()
+    pre = torch.randn(M, N, generator=gen).bfloat16()
+    same_kind(Q.q4_linear_backward(w, dy.cuda())["dx"], times(dy.double(), W.T), torch.bfloat16, "dx")
+    dz = R.linear_grad(W, dy.double(), pre.double(), "relu")[1]
+    dz = dz.bfloat16().double()                        # exact: dy or zero (an infinity times zero: NaN)
+    out = Q.q4_linear_backward(w, dy.cuda(), act=Q.Q4_ACT_RELU, pre=pre.cuda())
+    same_kind(out["dz"], dz, torch.bfloat16, "dz")
+    same_kind(out["dx"], times(dz, W.T), torch.bfloat16, "dx, relu")
+    # dh is finite, dh u is not: the row's largest value is met in u only
+    up = spoil(torch.randn(M, N, generator=gen) * 1e30, 1e38).bfloat16()
+    dh = torch.ones(M, N).bfloat16()
+    gate = (torch.rand(M, N, generator=gen) + 0.5).bfloat16()
+    out = Q.q4_gated_backward(w, u, dh.cuda(), gate.cuda(), up.cuda(), act=Q.Q4_ACT_RELU)
+    dup = gate.double()
+    same_kind(out["dgate"], up.double(), torch.bfloat16, "dgate")
+    same_kind(out["dx"], times(up.double(), W.T) + times(dup, U.T), torch.bfloat16, "dx, gated")
