@@ -146,7 +146,11 @@ __device__ __forceinline__ float activate(float z, float& slope) {
         constexpr float c = 1.59576912160573f;     // 2 sqrt(2 / pi)
         const float z2 = z * z;
         const float s = sigmoid(c * z * fmaf(0.044715f, z2, 1.0f));
-        if constexpr (GRAD) slope = fmaf(z * c * fmaf(0.134145f, z2, 1.0f), s * (1.0f - s), s);
+        if constexpr (GRAD) {
+            // s (1 - s) is zero from |z| = 16 on (and far before), where the cubic may overflow later
+            const float b = __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f);
+            slope = fmaf(b * c * fmaf(0.134145f, b * b, 1.0f), s * (1.0f - s), s);
+        }
         return z * s;
     } else if constexpr (ACT == ACT_RELU) {
         if constexpr (GRAD) slope = z > 0.0f ? 1.0f : 0.0f;

@@ -147,3 +147,25 @@ def test_infinities_in_gradients(fmt, M):
     dup = gate.double()
     same_kind(out["dgate"], up.double(), torch.bfloat16, "dgate")
     same_kind(out["dx"], times(up.double(), W.T) + times(dup, U.T), torch.bfloat16, "dx, gated")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_slopes_of_every_size(act):
+    """dz = dy act'(pre) for pre of either sign over bfloat16's range: where the slope has
+    reached 0 or 1, and where pre^3 leaves binary32's range."""
+    bits = torch.arange(0, 0x7F80, dtype=torch.int32)
+    pre = torch.cat([bits, bits + 0x8000 - (1 << 16)]).to(torch.int16).view(torch.bfloat16).view(-1, 64)
+    M = pre.shape[0]
+    w, _ = G.weight("q4_0", 64, 64, 1)
+    dz = Q.q4_linear_backward(w, torch.ones(M, 64).bfloat16().cuda(), act=G.ACTS[act], pre=pre.cuda())["dz"].double().cpu()
+    z = pre.double().clamp(-1e3, 1e3)                     # the slopes there are 0 and 1 to 1e-400
+    want = R.act(z, act)[1]
+    # half a unit of the rounding, 1.5e-7 of GELU's distribution function times two, binary32's own
+    assert ((dz - want).abs() <= 2.0 ** -8 * want.abs() + 1e-6).all(), (pre.flatten()[((dz - want).abs() - 2.0 ** -8 * want.abs()).argmax()])
+    one = torch.ones(M, 64).bfloat16().cuda()
+    gated = Q.q4_gated_backward(w, w, one, pre.cuda(), one, act=G.ACTS[act])
+    assert torch.equal(gated["dgate"].double().cpu(), dz)
+    value = R.act(z, act)[0]
+    value = torch.where(pre.double() > 1e3, pre.double(), value)
+    got = gated["dup"].double().cpu()
+    assert ((got - value).abs() <= 2.0 ** -8 * value.abs() + 1e-6).all()
