@@ -309,7 +309,7 @@ static void launch_shape(int epi, const TileArgs& a, unsigned grid, hipStream_t 
 
 hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s) {
     const int64_t threads = a.epi.M * ((a.epi.N + 7) / 8);
-    if ((threads + 255) / 256 > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable((threads + 255) / 256, 256)) return hipErrorInvalidValue;
     const dim3 grid((unsigned)((threads + 255) / 256));
     if (nmat == 2) hipLaunchKernelGGL((k_tile_join<EPI_GATED>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_tile_join<EPI_LINEAR>), grid, dim3(256), 0, s, a);
@@ -323,7 +323,7 @@ hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& args, h
     const int epi = p.parts > 1 ? EPI_PARTIAL : last;
     const int64_t tiles =
         ((a.w_panels + 2 * p.nt - 1) / (2 * p.nt)) * ((a.x_panels + 2 * p.mt - 1) / (2 * p.mt)) * p.parts;
-    if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launchable(tiles, 256)) return hipErrorInvalidValue;
     if (p.nt == 4 && p.mt == 4) launch_shape<4, 4>(epi, a, (unsigned)tiles, s);
     else if (p.nt == 4) launch_shape<4, 2>(epi, a, (unsigned)tiles, s);
     else if (p.mt == 4) launch_shape<2, 4>(epi, a, (unsigned)tiles, s);

@@ -20,9 +20,12 @@ namespace q4 {
 
 constexpr int kUnit = 1024;                 // bytes of a unit
 
-// Slices of a sum over K terms, and an image's bytes.
+// Slices of a sum over K terms.
 inline int64_t image_slices(int64_t K) { return (K + 31) / 32 * 2; }
-inline int64_t image_bytes(int64_t rows, int64_t slices) { return (rows + 31) / 32 * slices * kUnit; }
+
+// A launch has less than 2^32 threads along a dimension; one with more runs,
+// without an error, on what is left of them modulo 2^32.
+inline bool launchable(int64_t blocks, int threads) { return blocks * threads < int64_t(1) << 32; }
 
 // Epilogue of the product (one of them is chosen at compile time).
 enum : int {

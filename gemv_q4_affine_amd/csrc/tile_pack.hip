@@ -200,13 +200,13 @@ static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K
     if (!transposed) {
         constexpr int kGroupK = WF == WF_AFFINE8 ? 512 : 1024;
         const int64_t kgroups = (K + kGroupK - 1) / kGroupK, blocks = (N + 31) / 32 * mats * kgroups;
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(blocks, 256)) return hipErrorInvalidValue;
         hipLaunchKernelGGL((rest ? k_pack_weights<WF, true> : k_pack_weights<WF, false>), dim3((unsigned)blocks), dim3(256), 0,
                            s, w[0], w[mats - 1], mats, (int)N, K, image_slices(K) * (rest ? 2 : 1), kgroups, img);
     } else {
         constexpr int kTileK = WF == WF_AFFINE8 ? 128 : 256;
         const int64_t ktiles = (K + kTileK - 1) / kTileK, ntiles = (N + 63) / 64, blocks = ktiles * ntiles * mats;
-        if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!launchable(blocks, 256)) return hipErrorInvalidValue;
         hipLaunchKernelGGL((k_pack_weights_t<WF>), dim3((unsigned)blocks), dim3(256), 0, s, w[0], w[mats - 1], (int)N, K,
                            image_slices(N) * mats, ktiles, ntiles, img);
     }
@@ -301,12 +301,20 @@ __global__ __launch_bounds__(kPackThreads) void k_pack_rows(const void* __restri
 
 // Rows of a workgroup: four where eight would leave CUs idle.
 static int pack_rows(int64_t M) { return M > 8 * (current_cu_count() - 1) ? 8 : 4; }
+// Rows of a launch: a thread for each 1/128 row stays below a launch's 2^32
+// (whole panels, and whole groups of rows).
+constexpr int64_t kLaunchRows = int64_t(1) << 24;
 
 hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool twice, uint8_t* img, int8_t* xexp,
                          hipStream_t s) {
     const int rows = pack_rows(M);
-    hipLaunchKernelGGL(rows == 8 ? k_pack_rows<8> : k_pack_rows<4>, dim3((unsigned)((M + rows - 1) / rows)),
-                       dim3(kPackThreads), 0, s, x, dtype, M, K, image_slices(K) * (twice ? 2 : 1), twice ? 1 : 0, img, xexp);
+    const int64_t slices = image_slices(K) * (twice ? 2 : 1);
+    for (int64_t m = 0; m < M; m += kLaunchRows) {
+        const int64_t count = M - m < kLaunchRows ? M - m : kLaunchRows;
+        hipLaunchKernelGGL(rows == 8 ? k_pack_rows<8> : k_pack_rows<4>, dim3((unsigned)((count + rows - 1) / rows)),
+                           dim3(kPackThreads), 0, s, static_cast<const char*>(x) + m * K * 2, dtype, count, K, slices,
+                           twice ? 1 : 0, img + m / 32 * slices * kUnit, xexp + m);
+    }
     return hipGetLastError();
 }
 
@@ -443,10 +451,21 @@ int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N) { return (M + pack_rows(
 
 hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s) {
     const int rows = pack_rows(a.M);
-    const int64_t groups = (a.M + rows - 1) / rows;
+    const int64_t groups = (a.M + rows - 1) / rows, slices = image_slices(a.N);
     auto k = a.N % 8 == 0 ? (rows == 8 ? k_pack_dz<true, 8> : k_pack_dz<true, 4>)
                           : (rows == 8 ? k_pack_dz<false, 8> : k_pack_dz<false, 4>);
-    hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(kPackThreads), 0, s, a, image_slices(a.N), img, xexp, sums);
+    for (int64_t m = 0; m < a.M; m += kLaunchRows) {
+        LinearGradArgs t = a;
+        auto from = [&](const void* p) { return p ? const_cast<char*>(static_cast<const char*>(p)) + m * a.N * 2 : nullptr; };
+        t.M = a.M - m < kLaunchRows ? a.M - m : kLaunchRows;
+        t.dy = from(a.dy);
+        for (int i = 0; i < 2; i++) {
+            t.pre[i] = from(a.pre[i]);
+            t.dz[i] = from(a.dz[i]);
+        }
+        hipLaunchKernelGGL(k, dim3((unsigned)((t.M + rows - 1) / rows)), dim3(kPackThreads), 0, s, t, slices,
+                           img + m / 32 * slices * a.nmat * kUnit, xexp + m, sums + m / rows * a.nmat * a.N);
+    }
     if (a.dbias[0] || a.dbias[1])
         hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(1024), 0, s, sums, groups, a.nmat,
                            a.N, a.dbias[0], a.dbias[1]);

@@ -43,3 +43,26 @@ def test_a_dz_that_would_be_dy_is_refused():
     dz = torch.zeros_like(dy)
     out = Q.q4_linear_backward(w, dy, act=Q.Q4_ACT_RELU, pre=dy, dz=dz)
     assert out["dz"] is dz and torch.equal(dz, dy)
+
+
+def test_more_rows_than_one_launch_of_the_packers():
+    """2^25 rows and more: the row packers' 1024 threads for each eight rows pass 2^32."""
+    M, N, K = (1 << 25) + 4 * 1024 + 40, 8, 64
+    gen = torch.Generator("cuda").manual_seed(1)
+    w = Q.q4_quantize(torch.randn(N, K, device="cuda", generator=gen))
+    x = torch.randn(M, K, device="cuda", generator=gen, dtype=torch.bfloat16)
+    y = Q.q4_linear(w, x)
+    ends = [slice(0, 128), slice((1 << 24) - 64, (1 << 24) + 64), slice(M - 128, M)]
+    for part in ends:
+        assert torch.equal(y[part], Q.q4_linear(w, x[part].contiguous())), part
+    del x
+    pre = torch.randn(M, N, device="cuda", generator=gen, dtype=torch.bfloat16)
+    out = Q.q4_linear_backward(w, y, act=Q.Q4_ACT_SILU, pre=pre, bias_grad=True)
+    for part in ends:
+        small = Q.q4_linear_backward(w, y[part].contiguous(), act=Q.Q4_ACT_SILU, pre=pre[part].contiguous())
+        assert torch.equal(out["dx"][part], small["dx"]) and torch.equal(out["dz"][part], small["dz"]), part
+    # dz as it was summed, before its rounding; binary32 sums of 2^25 terms in groups of eight, then in order
+    s = torch.sigmoid(pre.double())
+    want = (y.double() * s * (1 + pre.double() * (1 - s))).sum(0)
+    size = (y.double() * s * (1 + pre.double() * (1 - s))).square().sum(0).sqrt()
+    assert ((out["dbias"].double() - want).abs() <= 1e-3 * size + 1e-6 * want.abs()).all()
