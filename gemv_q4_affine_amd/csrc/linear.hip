@@ -81,17 +81,24 @@ TileArgs tile_args(const Layout& l, uint8_t* ws) {
 // Column tiles of a workgroup: one pair at q4_gated (12288 x 4096: 17.6 us at
 // one row against 18.1 with three pairs, 41.0 at 32 rows against 42.7 with two).
 // At q4_linear two where they fill the CUs (8192 x 4096, 32 rows: 15.6 against 19.2
-// with one; 512 x 12288 in 8 parts: 9.0, with one 7.8), three up to four rows, and
-// above where they make one round over the CUs of three (12288 x 4096, affine4, 32 rows:
-// 18.2 against 21.0 with two; Q4_0, 16 rows, 13.6 against 14.6; 8 bits the same).
+// with one; 512 x 12288 in 8 parts: 9.0, with one 7.8).  Three, of which a CU holds
+// one workgroup, where they make one round over the CUs and two would make a
+// ragged one: more than two tiles a CU and at most three.  K = 4096, Q4_0, 16 rows:
+// N = 8448 12.3 us against 13.7 with two, 12288 13.8 against 14.6, but 16384 23.2
+// against 15.1; 32 rows 17.1 against 20.4, 19.2 / 21.1, 33.5 / 22.6; one row (K = 2048)
+// 6.4 / 7.0, 6.9 / 7.3, 11.3 / 8.0, and 31.0 / 22.9 at N = 65536.  At 8 bits only at
+// 5 to 16 rows (K = 2048, N = 8448, 16 rows 9.9 / 10.7; one row 9.7 / 9.3, and 32 rows
+// 16.1 / 13.8, where the accumulators beside two dwords of codes spill).
 // Eight waves where the workgroups do not outnumber the CUs (4096 x 4096 gated, 32
 // rows: 16.4 against 20.8 with four).
 FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
     const int64_t step = wf == WF_AFFINE8 ? 128 : 256, steps = (K + step - 1) / step;
     const int64_t tiles = (N + 15) / 16, cus = current_cu_count(), pairs = (tiles + 1) / 2;
     const int64_t most = M > 4 && steps >= 32 ? steps / 8 : 1;
+    const bool fills = most > 1 ? pairs * most >= cus : tiles > cus;
+    const bool three = most == 1 && tiles > 2 * cus && tiles <= 3 * cus && few_three(wf, M);
     FewPlan p{};
-    p.tiles = nmat == 2 || (most > 1 ? pairs * most < cus : tiles <= cus) ? 1 : tiles <= 2 * cus || (M > 4 && (most > 1 || tiles > 3 * cus)) ? 2 : 3;
+    p.tiles = nmat == 2 || !fills ? 1 : three ? 3 : 2;
     const int64_t groups = (tiles + p.tiles - 1) / p.tiles, room = 2 * cus / groups;
     const int64_t parts = room < 1 ? 1 : room < most ? room : most;
     p.per = (int)((steps + parts - 1) / parts);

@@ -614,6 +614,8 @@ struct FewPlan {
     int tiles, waves, parts, per;
 };
 FewPlan plan_few(int wf, int nmat, int64_t M, int64_t N, int64_t K);
+// Rows at which three column tiles a workgroup are there (measured at plan_few).
+constexpr bool few_three(int wf, int64_t M) { return wf != WF_AFFINE8 || (M > 4 && M <= 16); }
 // What takes the factor off the sums of a split again.
 inline float few_unit(int wf, int dtype) {
     return dtype != DT_BF16 ? 1.0f : (float)(1 << (wf == WF_AFFINE8 ? few::kDown<WF_AFFINE8, DT_BF16> : few::kDown<WF_Q4_0, DT_BF16>));
@@ -638,7 +640,7 @@ void few_tiles(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hip
     if (a.nmat == 2) few_waves<WF, XDT, MT, 1, true, DIAG>(a, p, split, s);
     else if (p.tiles == 1) few_waves<WF, XDT, MT, 1, false, DIAG>(a, p, split, s);
     else if (p.tiles == 2) few_waves<WF, XDT, MT, 2, false, DIAG>(a, p, split, s);
-    else few_launch<WF, XDT, MT, 3, false, DIAG, 8>(a, p, split, s);      // one workgroup a CU, or up to four rows
+    else if constexpr (few_three(WF, DIAG ? 1 : MT * 16)) few_launch<WF, XDT, MT, 3, false, DIAG, 8>(a, p, split, s);   // one workgroup a CU
 }
 template <int WF, int XDT>
 void few_rows(const LinearArgs& a, const FewPlan& p, const FewSplit& split, hipStream_t s) {
