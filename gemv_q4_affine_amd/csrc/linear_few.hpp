@@ -41,9 +41,11 @@
 // For q4_gated the tiles come in pairs, gate and up of the same 16 columns.  A
 // long sum over few columns is split over workgroups (FewSplit) and joined.
 //
-// Bound: memory at 1 to 16 rows (each weight byte is read once).  Measured, Q4_0,
-// N = 12288, K = 4096: one row 9.5 us (28.3 MB; with no loads at all 4.4), 16
-// rows 13.6, 32 rows 18.5; the gated pair 17.6, 22.6 and 41.
+// Bound: up to four rows by round trips to memory, with one step of a wave in flight;
+// above them by vector work, 16 to 18 instructions beside each MFMA, and by x through
+// LDS.  Measured, Q4_0, N = 12288, K = 4096: one row 9.7 us (28.3 MB, 2.9 TB/s; with no loads
+// at all 4.4), 16 rows 13.8 (2.1 TB/s), 32 rows 19.0; affine 8, one row 16.3; the
+// gated pair 18.0, 23.2 and 41.5.
 #pragma once
 
 #include "block_common.hpp"

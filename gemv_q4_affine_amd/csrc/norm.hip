@@ -8,8 +8,9 @@
 // stay in its registers, and the gradients' sums over the rows with them.
 //
 // Measured, D = 4096 bfloat16, RMS norms before and after, a gate: forward 17 us
-// at 2048 rows, 57 us at 8192 (4.7 of the 5.1 TB/s a large copy moves);
-// gradients 101 us at 8192 rows (4.0 TB/s) and 7 us for the sums' join.  What
+// at 2048 rows, 53 us at 8192 (5.1 TB/s, a large copy's rate); gradients 102 us
+// at 8192 rows (4.0 TB/s) and 7 us for the sums' join.  With one RMS norm and no gate
+// 49 and 88 us at 8192 rows, the gradients with their join.  What
 // cost most on the way: registers.  With the weights held in binary32 and the
 // absent tensors' cases compiled in, the gradients took 205 registers, one
 // workgroup a CU and 118 us, and bounded to 128 they spilled 108 (258 us); rows
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(1024, V == 1 ? 5 : 4) void k_block_norm(const NormA
 // first and its last, kept at [workgroup][2][D] for k_norm_join.
 
 // Forms compiled apart, with every tensor there, for registers: the norms after
-// and before the block, and the one before it only (1000 x 1537, bfloat16: 8.9 us
+// and before the block, and the one before it only (1000 x 1537, bfloat16: 9.2 us
 // against 22.3 in the general form, which spills).
 enum : int { FORM_ANY = 0, FORM_BOTH = 1, FORM_PRE = 2 };
 

@@ -21,13 +21,19 @@
  * codes, scales, biases, group 64) get no gradient.
  *
  * dtype: Q4_BF16 or Q4_F16, the type of every activation tensor of the call.
- * Products are exact or binary16 x binary16 with binary32 accumulation
- * (weights dequantised to binary16, rounding <= 2^-11, absolute 2^-25 below
- * 2^-14; x scaled per row by a power of two so that the whole bfloat16 range
- * fits; for binary16 outputs of a gated product or under a curved activation the
- * roundings' remainders are summed too); biases, activations,
- * products of projections, residuals and norms are computed in binary32 and
- * rounded once into the output.  The dequantised weights must fit binary16.
+ * Up to 64 rows the forward products are exact with binary32 accumulation.  Above, and
+ * in the gradients, they are binary16 x binary16 (weights dequantised to
+ * binary16, rounding <= 2^-11, absolute 2^-25 below 2^-14: the dequantised weights
+ * must fit binary16; x and dz scaled per row by a power of two); for binary16 outputs of
+ * a gated product or under a curved activation the roundings' remainders are
+ * summed too.  Either way x and dz may be anything in their type's range.  Biases,
+ * activations, products of projections, residuals and norms are computed in
+ * binary32 and rounded once into the output.
+ *
+ * A row of x (dz, r, y) with an infinity or a NaN spoils no other row of the
+ * outputs.  Its own sums over k are what their infinite terms make them: an infinity
+ * of their sign, NaN where they oppose each other, where the weight is zero
+ * (above 64 rows and in the gradients: zero in binary16), or next to a NaN.
  */
 #ifndef GEMV_Q4_AFFINE_AMD_Q4_BLOCK_H
 #define GEMV_Q4_AFFINE_AMD_Q4_BLOCK_H
@@ -120,6 +126,7 @@ int q4_gated_backward(int fmt, const uint8_t* gate_q, const uint16_t* gate_s, co
  *   p = post(y);  r' = r + scale * gate * p;  n = pre(r')
  * with post and pre one of Q4_NORM_*.  n is computed from r' before r' is
  * rounded into r_out.
+ * Squares are summed in binary32: a row whose sum of squares passes 3.4e38 has rstd 0.
  *   y       : device, [M][D] of dtype, a block's output, or NULL (then r' = r,
  *             post_norm is Q4_NORM_NONE, gate and r_out are NULL: the norm
  *             before the first block)
