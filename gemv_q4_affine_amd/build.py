@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libq4.so")
 
 SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "gemm_big.hip", "gemm_q8.hip", "affine8.hip", "noalloc.hip",
            "capi.cpp", "block_capi.cpp", "linear.hip", "linear_few_q4_0.hip", "linear_few_affine4.hip",
-           "linear_few_affine8.hip", "tile_gemm.hip", "tile_pack.hip", "norm.hip"]
+           "linear_few_affine8.hip", "tile_gemm.hip", "tile_pack.hip", "norm.hip", "mx_capi.cpp", "mx_quant.hip",
+           "mx_norm.hip", "mx_linear.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -128,7 +129,7 @@ def _compile_san(src: str) -> str:
 
 def build_host_sanitized(verbose: bool = False) -> str:
     """Build SAN_LIB if any source is newer than it; return its path."""
-    srcs = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in ("q4.h", "q4_block.h")]
+    srcs = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in ("q4.h", "q4_block.h", "q4_mx.h")]
     if os.path.exists(SAN_LIB) and os.path.getmtime(SAN_LIB) >= max(os.path.getmtime(f) for f in srcs):
         return SAN_LIB
     os.makedirs(SAN_DIR, exist_ok=True)

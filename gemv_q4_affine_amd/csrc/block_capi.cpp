@@ -7,34 +7,15 @@
 
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
 #include "block_common.hpp"
+#include "capi_checks.hpp"
 
 namespace {
 
-constexpr int64_t kMaxDim = int64_t(1) << 30;
-// N and K: a panel of 32 rows of an operand image stays below 2^32 bytes
-constexpr int64_t kMaxSum = int64_t(1) << 25;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int need(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (!p) return Q4_ERR_NULL;
-    for (const void* p : ps)
-        if (!aligned16(p)) return Q4_ERR_ALIGN;
-    return Q4_OK;
-}
-int optional(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (!aligned16(p)) return Q4_ERR_ALIGN;
-    return Q4_OK;
-}
+using namespace q4::checks;
 
 bool fmt_ok(int fmt) { return fmt == Q4_FMT_Q4_0 || fmt == Q4_FMT_AFFINE4 || fmt == Q4_FMT_AFFINE8; }
-bool act_ok(int act) { return act >= Q4_ACT_NONE && act <= Q4_ACT_RELU; }
-bool norm_ok(int norm) { return norm >= Q4_NORM_NONE && norm <= Q4_NORM_LAYER; }
 
 int format_wf(int fmt) {
     return fmt == Q4_FMT_Q4_0 ? q4::WF_Q4_0 : fmt == Q4_FMT_AFFINE4 ? q4::WF_AFFINE4 : q4::WF_AFFINE8;
@@ -51,15 +32,6 @@ int check_planes(int fmt, const void* q, const void* s, const void* b) {
     const int rc = need({q, s});
     return rc || fmt == Q4_FMT_Q4_0 ? rc : need({b});
 }
-
-int check_workspace(const void* ws, int64_t have, int64_t want) {
-    if (want <= 0) return Q4_OK;
-    if (!ws || have < want) return Q4_ERR_WORKSPACE;
-    return aligned16(ws) ? Q4_OK : Q4_ERR_ALIGN;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? Q4_OK : Q4_ERR_HIP; }
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 int64_t forward_bytes(int fmt, int nmat, int dtype, int64_t M, int64_t N, int64_t K) {
     if (dtype != Q4_BF16 && dtype != Q4_F16) return 0;
@@ -214,16 +186,6 @@ int q4_gated_backward(int fmt, const uint8_t* gate_q, const uint16_t* gate_s, co
 }
 
 // ---- norms ---------------------------------------------------------------------
-
-static int check_norm(int dtype, int r_dtype, int64_t M, int64_t D, int64_t gate_rows, float scale, int post_norm,
-                      int pre_norm) {
-    if (dtype != Q4_BF16 && dtype != Q4_F16 && dtype != Q4_F32) return Q4_ERR_DTYPE;
-    if (r_dtype != dtype && r_dtype != Q4_F32) return Q4_ERR_DTYPE;
-    if (M < 0 || D < 0 || M > kMaxDim || D > Q4_NORM_MAX_D) return Q4_ERR_SHAPE;
-    if (!norm_ok(post_norm) || !norm_ok(pre_norm) || !std::isfinite(scale)) return Q4_ERR_ARG;
-    if (gate_rows < 1 && M > 0) return Q4_ERR_ARG;
-    return Q4_OK;
-}
 
 int block_norm(const void* y, const void* r, int dtype, int r_dtype, int64_t M, int64_t D, int post_norm,
                const void* post_weight, const void* post_bias, const void* gate, int64_t gate_rows, float scale,

@@ -58,7 +58,7 @@ hipError_t launch_q4_gemv_multi(int nmat, const uint8_t* const* qs, const uint16
 
 // GEMM paths.  fmt: 0 = Q4_0 planes (a = qs, b = d), 1 = affine (a = q,
 // b = scales, c = biases), 2 = dense binary16 W (a = w).
-enum : int { WF_Q4_0 = 0, WF_AFFINE4 = 1, WF_DENSE16 = 2, WF_AFFINE8 = 3 };
+enum : int { WF_Q4_0 = 0, WF_AFFINE4 = 1, WF_DENSE16 = 2, WF_AFFINE8 = 3, WF_MXFP4 = 4 };
 
 hipError_t launch_gemm_mfma(int wfmt, const void* a, const void* b, const void* c,
                             const void* x, int xdt, void* y, int ydt,

@@ -46,9 +46,9 @@ Layout forward_layout(int nmat, bool rest, int64_t M, int64_t N, int64_t K) {
 // two of a gated product and a curved activation's slope made it 1.6 to 1.8
 // (affine4, 200 rows), so there the remainders are summed too, at twice the matrix
 // work (12288 x 4096, 512 rows, gated: 291 us against 148).  bfloat16 outputs are
-// eight times coarser.
-bool sums_rest(int nmat, int dtype, int act) {
-    return dtype == DT_F16 && (nmat == 2 || (act != ACT_NONE && act != ACT_RELU));
+// eight times coarser, and MXFP4 weights are exact in binary16.
+bool sums_rest(int wf, int nmat, int dtype, int act) {
+    return wf != WF_MXFP4 && dtype == DT_F16 && (nmat == 2 || (act != ACT_NONE && act != ACT_RELU));
 }
 Layout backward_layout(int nmat, int64_t M, int64_t N, int64_t K) {
     const int64_t slices = image_slices(N) * nmat;
@@ -114,7 +114,7 @@ static int64_t few_part_row(int nmat, int64_t N) { return (N + 31) / 32 * nmat *
 int64_t linear_workspace_bytes(int wf, int nmat, int dtype, int64_t M, int64_t N, int64_t K) {
     if (M > kFewCallMaxM) {
         const int64_t one = forward_layout(nmat, false, M, N, K).total;
-        const int64_t two = dtype == DT_F16 ? forward_layout(nmat, true, M, N, K).total : 0;
+        const int64_t two = wf != WF_MXFP4 && dtype == DT_F16 ? forward_layout(nmat, true, M, N, K).total : 0;
         return one > two ? one : two;
     }
     const FewPlan p = plan_few(wf, nmat, few_rows_of(M), N, K);
@@ -172,7 +172,7 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
         t.epi = epilogue_args(a);
         return launch_tile_join(a.nmat, t, s);
     }
-    const bool rest = sums_rest(a.nmat, a.dtype, a.act);
+    const bool rest = sums_rest(a.wf, a.nmat, a.dtype, a.act);
     const Layout l = forward_layout(a.nmat, rest, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, rest, ws, s);

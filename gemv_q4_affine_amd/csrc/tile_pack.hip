@@ -2,6 +2,7 @@
 // (tile_image.hpp): weights dequantised to binary16, by rows or transposed;
 // activations and gradients scaled to binary16 row by row.  All are bound by
 // memory (a quantised matrix read, two bytes a weight written).
+#include "mx_common.hpp"
 #include "tile_image.hpp"
 
 namespace q4 {
@@ -9,7 +10,8 @@ namespace q4 {
 // ---- weights ---------------------------------------------------------------------
 //
 // Dequantised exactly in binary32 ((q - 8) d has 15 bits, q s + b one rounding)
-// and rounded once to binary16.
+// and rounded once to binary16; MXFP4 codes are converted straight to binary16,
+// which holds them exactly at scales of 2^-23 to 2^13.
 
 // Codes as binary32: byte e of w (8-bit), or its low / high nibble.
 template <int E>
@@ -22,10 +24,19 @@ struct RowScale {
         return WF == WF_Q4_0 ? (q - 8.0f) * s : __builtin_fmaf(q, s, b);
     }
 };
+// MXFP4: the eight codes of a word as four pairs of binary16.
+__device__ __forceinline__ u32x4_t mx_pairs(uint32_t w, float s) {
+    return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
+}
 template <int WF>
 __device__ __forceinline__ RowScale<WF> row_scale(const QuantW& w, int64_t n, int64_t blk32, int64_t K) {
     if constexpr (WF == WF_Q4_0) {
         return {f16_to_f32(w.s[n * (K / 32) + blk32]), 0.0f};
+    } else if constexpr (WF == WF_MXFP4) {
+        return {mx_scale(reinterpret_cast<const uint8_t*>(w.s)[n * (K / 32) + blk32]), 0.0f};
     } else {
         const int64_t g = n * (K / 64) + (blk32 >> 1);
         return {bf16_to_f32(w.s[g]), bf16_to_f32(w.b[g])};
@@ -86,6 +97,10 @@ __global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int 
         uint8_t* out = img + (panel * slices + 2 * b) * kUnit + j * 16;
 #pragma unroll
         for (int c = 0; c < 4; c++) {        // elements 8 c .. 8 c + 7: slice c / 2, half c % 2
+            if constexpr (WF == WF_MXFP4) {
+                *reinterpret_cast<u32x4_t*>(out + (c >> 1) * kUnit + (c & 1) * 512) = mx_pairs(raw[0][c], sc[t].s);
+                continue;
+            }
             float f[8];
             uint32_t lo, hi;
             if constexpr (WF == WF_AFFINE8) {
@@ -164,7 +179,20 @@ __global__ __launch_bounds__(256) void k_pack_weights_t(QuantW w0, QuantW w1, in
         for (int i = 0; i < 8; i++) f[i] = sc[i](code(raw[i]));
         *reinterpret_cast<u32x4_t*>(base + j * 16) = pack8(DT_F16, f);
     };
-    if constexpr (WF == WF_AFFINE8) {
+    if constexpr (WF == WF_MXFP4) {
+        // elements 8 wb .. + 7 of the eight rows, two rows to a word
+        u32x4_t pair[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) pair[i] = mx_pairs(raw[i], sc[i].s);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            u32x4_t v;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                v[i] = __builtin_amdgcn_perm(pair[2 * i + 1][e >> 1], pair[2 * i][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+            *reinterpret_cast<u32x4_t*>(base + (8 * wb + e) * 16) = v;
+        }
+    } else if constexpr (WF == WF_AFFINE8) {
         put(4 * wb + 0, [](uint32_t v) { return byte_f32<0>(v); });
         put(4 * wb + 1, [](uint32_t v) { return byte_f32<1>(v); });
         put(4 * wb + 2, [](uint32_t v) { return byte_f32<2>(v); });
@@ -201,7 +229,9 @@ static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K
         constexpr int kGroupK = WF == WF_AFFINE8 ? 512 : 1024;
         const int64_t kgroups = (K + kGroupK - 1) / kGroupK, blocks = (N + 31) / 32 * mats * kgroups;
         if (!launchable(blocks, 256)) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((rest ? k_pack_weights<WF, true> : k_pack_weights<WF, false>), dim3((unsigned)blocks), dim3(256), 0,
+        auto k = k_pack_weights<WF, false>;
+        if constexpr (WF != WF_MXFP4) k = rest ? k_pack_weights<WF, true> : k;
+        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), 0,
                            s, w[0], w[mats - 1], mats, (int)N, K, image_slices(K) * (rest ? 2 : 1), kgroups, img);
     } else {
         constexpr int kTileK = WF == WF_AFFINE8 ? 128 : 256;
@@ -217,6 +247,7 @@ hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int
                                uint8_t* img, hipStream_t s) {
     if (wf == WF_Q4_0) return pack_weights_t<WF_Q4_0>(mats, w, N, K, transposed, rest, img, s);
     if (wf == WF_AFFINE4) return pack_weights_t<WF_AFFINE4>(mats, w, N, K, transposed, rest, img, s);
+    if (wf == WF_MXFP4) return pack_weights_t<WF_MXFP4>(mats, w, N, K, transposed, rest, img, s);
     return pack_weights_t<WF_AFFINE8>(mats, w, N, K, transposed, rest, img, s);
 }
 

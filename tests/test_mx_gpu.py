@@ -1,0 +1,473 @@
+"""The operators on microscaled numbers (mx_quantize, mx_linear, mx_gated, their
+gradients, block_norm_mx) on the GPU against binary64 (mx_reference,
+block_reference).
+
+Tolerances, from the arithmetic (relative 2-norms):
+  * an output rounded once into its type is within u of its value, u = 2^-8
+    (bfloat16), 2^-11 (binary16), 2^-24 (binary32); below binary16's normal range
+    within 2^-25 absolutely.
+  * binary32 sums of n terms: about sqrt(n) 2^-24, below 2^-17 here.
+  * MXFP8 x: a matrix instruction cuts the 64 or 128 products of a step 2^-16 below
+    the largest of them, each by up to that: over a sum at most about
+    sqrt(128) 2^-16 of a largest product, 2^-12 of the sum where terms are of
+    like size.
+  * 16-bit x above 64 rows, and dz in the gradients: binary16 operands, 2^-11 each.
+  * codes and scales: equal.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import block_reference as R
+import gemv_q4_affine_amd as Q
+import mx_reference as X
+
+pytestmark = pytest.mark.gpu
+
+ACTS = {"none": Q.Q4_ACT_NONE, "silu": Q.Q4_ACT_SILU, "gelu": Q.Q4_ACT_GELU, "gelu_tanh": Q.Q4_ACT_GELU_TANH,
+        "relu": Q.Q4_ACT_RELU}
+NORMS = {"none": Q.Q4_NORM_NONE, "rms": Q.Q4_NORM_RMS, "layer": Q.Q4_NORM_LAYER}
+TYPES = {"fp4": Q.Q4_MXFP4, "fp8": Q.Q4_MXFP8}
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+F32 = 2.0 ** -17
+XS = ["bf16", "f16", "fp8", "fp4"]
+
+
+@pytest.fixture(autouse=True)
+def _done():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    yield
+    torch.cuda.synchronize()
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def bar(dtype, x="bf16"):
+    return U[dtype] + F32 + (2.0 ** -12 if x == "fp8" else 2.0 ** -11 if x in DT else 0.0)
+
+
+def near(got, want, limit, what):
+    """Values past the type's range (by more than `limit`) are infinities; the others' 2-norms."""
+    got, top = got.cpu(), torch.finfo(got.dtype).max
+    past, inside = want.abs() > top * (1 + limit), want.abs() < top * (1 - limit)
+    assert torch.equal(got[past], (want[past].sign() * math.inf).to(got.dtype)), what
+    if got.shape == want.shape and not inside.all():
+        got, want = got[inside], want[inside]
+    e = R.rel(got, want)
+    if got.dtype == torch.float16 and want.norm() > 0:
+        limit += 2.0 ** -25 * want.numel() ** 0.5 / want.norm().item()
+    say(f"  {what}: {e:.3g} (limit {limit:.3g})")
+    assert tuple(got.shape) == tuple(want.shape), what
+    assert e <= limit, f"{what}: {e} > {limit}"
+
+
+def cuda(planes):
+    return tuple(t.cuda() for t in planes)
+
+
+def weight(N, K, seed, scale=0.02):
+    p, v = X.tensor(N, K, "fp4", seed, scale, spread=1)
+    return cuda(p), v
+
+
+def rand(gen, *shape, dtype=torch.bfloat16, scale=1.0, mean=0.0):
+    t = (torch.randn(*shape, generator=gen) * scale + mean).to(dtype)
+    return t.cuda(), t.double()
+
+
+def activation(gen, M, K, x, seed=0):
+    if x in DT:
+        return rand(gen, M, K, dtype=DT[x])
+    p, v = X.tensor(M, K, x, seed, 1.0)
+    return cuda(p), v
+
+
+# ---- planes ----------------------------------------------------------------------
+
+def special(dtype):
+    """Rows of 32: zeros, borders between codes under several scales, ends of the range, infinities and NaN."""
+    info = torch.finfo(dtype)
+    rows = [np.zeros(32), -np.zeros(32)]
+    for kind in ("fp4", "fp8"):
+        t = np.unique(np.abs(X.table(kind)[np.isfinite(X.table(kind))]))
+        mid = (t[1:] + t[:-1]) / 2
+        for c in range(0, len(mid), 30):
+            for e in (0, -3, 5):
+                row = np.zeros(32)
+                row[:len(mid[c:c + 30])] = mid[c:c + 30] * np.where(np.arange(len(mid[c:c + 30])) % 2, -1, 1)
+                row[31] = t[-1] * 1.13                     # past the largest code, within its power of two
+                rows.append(row * 2.0 ** e)
+    low = np.full(32, info.smallest_normal)
+    low[1::2] /= 2
+    low[5] /= -4
+    rows += [low, low / 4, np.full(32, info.max), np.where(np.arange(32) % 3, 1.0, -info.max), np.linspace(-1, 1, 32) * info.tiny * 3]
+    for bad in (np.inf, -np.inf, np.nan):
+        row = np.linspace(-2, 2, 32)
+        row[17] = bad
+        rows.append(row)
+    return torch.from_numpy(np.stack(rows)).to(dtype)
+
+
+@pytest.mark.parametrize("kind", ["fp4", "fp8"])
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("M,K", [(0, 0), (1, 32), (3, 96), (17, 4096), (257, 2080), (1000, 32)])
+def test_quantize_codes(kind, dt, M, K):
+    say("quantize", kind, dt, M, K)
+    gen = torch.Generator().manual_seed(M + K)
+    v = special(DT[dt]) if M == 0 else (torch.randn(M, K, generator=gen) * torch.exp(2 * torch.randn(M, 1, generator=gen))).to(DT[dt])
+    codes, scales = Q.mx_quantize(v.cuda(), TYPES[kind])
+    c64, s64 = X.quantize(v.double().numpy(), kind)
+    assert np.array_equal(scales.cpu().numpy(), s64)
+    assert np.array_equal(X.unpacked(codes.cpu().numpy(), kind), c64)
+    back = Q.mx_dequantize((codes, scales), dtype=torch.float32).cpu().double().numpy()
+    assert np.array_equal(back, X.values(c64, s64, kind), equal_nan=True)
+
+
+@pytest.mark.parametrize("kind", ["fp4", "fp8"])
+@pytest.mark.parametrize("dt", list(DT))
+def test_dequantize_every_code_and_scale(kind, dt):
+    n = 16 if kind == "fp4" else 256
+    codes = np.tile(np.arange(n, dtype=np.uint8), (256, 32 // n if n < 32 else 1))
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], codes.shape[1] // 32, 1)
+    p = (torch.from_numpy(X.planes(codes, kind)).cuda(), torch.from_numpy(scales).cuda())
+    got = Q.mx_dequantize(p, dtype=DT[dt]).cpu()
+    want = torch.from_numpy(X.values(codes, scales, kind)).float().to(DT[dt])      # binary32 holds them but for overflow
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(7.0, math.inf, -math.inf), want.nan_to_num(7.0, math.inf, -math.inf))
+
+
+# ---- linear ----------------------------------------------------------------------
+
+SHAPES = [(1, 64, 32), (1, 37, 2048), (2, 300, 320), (3, 1, 96), (4, 2048, 8192), (5, 130, 544), (7, 129, 4096), (16, 512, 576),
+          (17, 33, 192), (32, 260, 1088), (33, 96, 64), (48, 64, 8192), (64, 255, 448), (65, 130, 128), (127, 512, 512), (130, 31, 2048),
+          (300, 523, 704), (512, 2048, 256), (1000, 136, 1984), (257, 1025, 160)]
+
+
+@pytest.mark.parametrize("x", XS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear(x, M, N, K):
+    gen = torch.Generator().manual_seed(M * 31 + N)
+    w, W = weight(N, K, M + N + K)
+    for act, bias, residual, save, dt in [("none", False, False, False, "bf16"), ("gelu", True, True, True, "bf16"),
+                                          ("silu", True, False, True, "f16")]:
+        if x in DT and x != dt:
+            continue
+        say(f"linear x={x} M={M} N={N} K={K} {act} {dt}")
+        xq, x64 = activation(gen, M, K, x, seed=M)
+        b, b64 = rand(gen, N, dtype=DT[dt]) if bias else (None, None)
+        r, r64 = rand(gen, M, N, dtype=DT[dt]) if residual else (None, None)
+        call = lambda: Q.mx_linear(w, xq, bias=b, act=ACTS[act], residual=r, save_pre=save, dtype=DT[dt])  # noqa: E731
+        got = call()
+        y64, z64 = R.linear(x64, W, b64, act, r64)
+        near(got[0] if save else got, y64, bar(DT[dt], x), "y")
+        if save:
+            near(got[1], z64, bar(DT[dt], x), "pre")
+        again = call()
+        assert torch.equal(again[0] if save else again, got[0] if save else got), "not deterministic"
+
+
+@pytest.mark.parametrize("x", XS)
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_linear_activations(x, act, M):
+    gen = torch.Generator().manual_seed(M)
+    dt = DT.get(x, torch.float16)
+    w, W = weight(192, 128, 5, scale=0.3)
+    xq, x64 = activation(gen, M, 128, x)
+    y, pre = Q.mx_linear(w, xq, act=ACTS[act], save_pre=True, dtype=dt)
+    y64, z64 = R.linear(x64, W, None, act, None)
+    # an activation's slope is at most 1.13, and its value's error that of z, which may be the larger
+    near(y, y64, bar(dt, x) * max(1.0, 1.13 * (z64.norm() / y64.norm()).item()), act)
+    near(pre, z64, bar(dt, x), "pre")
+
+
+@pytest.mark.parametrize("x", XS)
+@pytest.mark.parametrize("M", [1, 40, 150])
+def test_linear_residual_in_place_and_rows_behind(x, M):
+    gen = torch.Generator().manual_seed(M)
+    N, K = 160, 256
+    w, _ = weight(N, K, 1)
+    xq, _ = activation(gen, M, K, x)
+    dt = DT.get(x, torch.bfloat16)
+    r, _ = rand(gen, M + 3, N, dtype=dt)
+    want, behind = Q.mx_linear(w, xq, residual=r[:M], dtype=dt), r[M:].clone()
+    got = Q.mx_linear(w, xq, residual=r[:M], y=r[:M], dtype=dt)
+    assert got.data_ptr() == r.data_ptr() and torch.equal(got, want) and torch.equal(r[M:], behind)
+
+
+@pytest.mark.parametrize("x", XS)
+def test_empty_calls(x):
+    gen = torch.Generator().manual_seed(1)
+    w, _ = weight(64, 64, 1)
+    dt = DT.get(x, torch.bfloat16)
+    e, _ = activation(gen, 0, 64, x)
+    assert Q.mx_linear(w, e, dtype=dt).shape == (0, 64) and Q.mx_gated(w, w, e, dtype=dt).shape == (0, 64)
+    none = (w[0][:0], w[1][:0])
+    xq, _ = activation(gen, 5, 64, x)
+    assert Q.mx_linear(none, xq, dtype=dt).shape == (5, 0)
+    dy = torch.zeros(5, 0, device="cuda", dtype=torch.bfloat16)
+    assert not Q.mx_linear_backward(none, dy)["dx"].any()
+    g = Q.mx_linear_backward(w, torch.zeros(0, 64, device="cuda", dtype=torch.bfloat16), bias_grad=True)
+    assert g["dx"].shape == (0, 64) and not g["dbias"].any()
+
+
+# ---- gated -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("x", XS)
+@pytest.mark.parametrize("M,N,K", [(1, 64, 64), (1, 1000, 4096), (3, 33, 96), (4, 100, 8192), (5, 48, 1024), (16, 260, 544),
+                                   (19, 511, 2080), (64, 96, 256), (65, 64, 128), (130, 257, 480), (700, 520, 1056)])
+def test_gated(x, M, N, K):
+    gen = torch.Generator().manual_seed(M + N)
+    g, G = weight(N, K, 1, 0.04)
+    u, Uw = weight(N, K, 2, 0.04)
+    for act, bias, save, dt in [("silu", False, False, "bf16"), ("gelu", True, True, "f16"), ("relu", True, True, "bf16")]:
+        if x in DT and x != dt:
+            continue
+        say(f"gated x={x} M={M} N={N} K={K} {act} {dt}")
+        xq, x64 = activation(gen, M, K, x, seed=K)
+        bg, bg64 = rand(gen, N, dtype=DT[dt]) if bias else (None, None)
+        bu, bu64 = rand(gen, N, dtype=DT[dt]) if bias else (None, None)
+        got = Q.mx_gated(g, u, xq, act=ACTS[act], gate_bias=bg, up_bias=bu, save_pre=save, dtype=DT[dt])
+        h64, g64, u64 = R.gated(x64, G, Uw, bg64, bu64, act)
+        # two factors' errors; the activation may be smaller than its argument
+        grow = max(1.0, 1.13 * ((g64.abs() * u64.abs()).norm() / h64.norm()).item())
+        near(got[0] if save else got, h64, U[DT[dt]] + 2 * grow * (bar(DT[dt], x) - U[DT[dt]]), "h")
+        if save:
+            near(got[1], g64, bar(DT[dt], x), "g")
+            near(got[2], u64, bar(DT[dt], x), "u")
+
+
+# ---- gradients ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["none", "silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 32), (3, 33, 96), (40, 130, 544), (64, 96, 256), (200, 511, 480), (700, 256, 1056)])
+def test_linear_gradients(act, M, N, K):
+    gen = torch.Generator().manual_seed(M + K)
+    w, W = weight(N, K, 3)
+    dy, dy64 = rand(gen, M, N, scale=0.01)
+    pre, pre64 = rand(gen, M, N) if act != "none" else (None, None)
+    got = Q.mx_linear_backward(w, dy, act=ACTS[act], pre=pre, bias_grad=True)
+    dx, dz, db = R.linear_grad(W, dy64, pre64, act)
+    near(got["dx"], dx, bar(torch.bfloat16), "dx")
+    near(got["dbias"], db, 2 * F32, "dbias")
+    assert ("dz" in got) == (act != "none")
+    if act != "none":
+        near(got["dz"], dz, U[torch.bfloat16] + F32, "dz")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 32), (5, 33, 96), (70, 257, 544), (500, 128, 2080)])
+def test_gated_gradients(M, N, K):
+    gen = torch.Generator().manual_seed(M + K)
+    g, G = weight(N, K, 1)
+    u, Uw = weight(N, K, 2)
+    dh, dh64 = rand(gen, M, N, scale=0.01)
+    gp, gp64 = rand(gen, M, N)
+    up, up64 = rand(gen, M, N)
+    got = Q.mx_gated_backward(g, u, dh, gp, up, act=ACTS["silu"], bias_grad=True)
+    want = R.gated_grad(G, Uw, dh64, gp64, up64, "silu")
+    for k, v, limit in zip(("dx", "dgate", "dup", "dgate_bias", "dup_bias"), want, (bar(torch.bfloat16),) + (U[torch.bfloat16] + F32,) * 2 + (2 * F32,) * 2):
+        near(got[k], v, limit, k)
+
+
+@pytest.mark.parametrize("x", ["fp8", "fp4"])
+def test_gradient_against_differences(x):
+    """dx along a direction against the change of <dy, y>: y is linear in x's values, so differences are exact but for
+    the outputs' roundings, each within u of |y|."""
+    gen = torch.Generator().manual_seed(4)
+    M, N, K = 24, 160, 96
+    w, W = weight(N, K, 9, 0.2)
+    a, a64 = activation(gen, M, K, x, seed=1)
+    b, b64 = activation(gen, M, K, x, seed=2)
+    dy, dy64 = rand(gen, M, N)
+    dx = Q.mx_linear_backward(w, dy)["dx"].cpu().double()
+    ya, yb = (Q.mx_linear(w, t, dtype=torch.float16).cpu().double() for t in (a, b))
+    change = (dy64 * (yb - ya)).sum().item()
+    slack = ((dy64.abs() * (ya.abs() + yb.abs())).square().sum().sqrt() * (U[torch.float16] + 2.0 ** -12)
+             + ((b64 - a64).abs() * dx.abs()).square().sum().sqrt() * bar(torch.bfloat16)).item()
+    assert abs(change - (dx * (b64 - a64)).sum().item()) <= 4 * slack
+
+
+# ---- norm ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,D", [(1, 32), (1, 4096), (3, 96), (5, 2048), (33, 544), (600, 1056), (2, 8224), (3, 16416), (2, 32768)])
+def test_block_norm_mx(kind, M, D):
+    gen = torch.Generator().manual_seed(M + D)
+    for dt, rdt, pre, post, gates, bias in [("bf16", "bf16", "rms", "none", 0, False), ("f16", "f32", "layer", "layer", M, True),
+                                            ("bf16", "f32", "rms", "rms", 1, False), ("f32", "f32", "layer", "rms", 0, True),
+                                            ("f16", "f16", "rms", "layer", 1, True)]:
+        say(f"norm {kind} M={M} D={D} {dt} {rdt} {pre} {post} gates={gates}")
+        y, y64 = rand(gen, M, D, dtype=DT[dt])
+        r, r64 = rand(gen, M, D, dtype=DT[rdt], scale=2.0)
+        v = lambda on, **k: rand(gen, D, dtype=DT[dt], **k) if on else (None, None)  # noqa: E731
+        pw, pw64 = v(True, scale=0.1, mean=1.0)
+        pb, pb64 = v(bias, scale=0.1)
+        qw, qw64 = v(post != "none", scale=0.1, mean=1.0)
+        qb, qb64 = v(bias and post != "none", scale=0.1)
+        gate, gate64 = rand(gen, gates, D, dtype=DT[dt]) if gates else (None, None)
+        eps, scale = 1e-5, 0.5
+        eps64, scale64 = float(np.float32(eps)), float(np.float32(scale))
+        c = dict(pre=pre, post=post, pre_w=pw64, pre_b=pb64, post_w=qw64, post_b=qb64, scale=scale64, eps=eps64,
+                 gate=None if gate is None else gate64.repeat_interleave(M // gates, 0))
+        r1, n, st = R.block_norm(r64, y64, c)
+        got_r, (codes, scales), stats = Q.block_norm_mx(
+            r, y, pre_norm=NORMS[pre], pre_weight=pw, pre_bias=pb, post_norm=NORMS[post], post_weight=qw, post_bias=qb, gate=gate,
+            scale=scale, eps=eps, n_type=TYPES[kind], save_stats=True)
+        near(got_r, r1, U[DT[rdt]], "r")
+        near(stats, st, U[torch.float32], "stats")
+        c64, s64 = X.quantize(n.numpy(), kind)
+        assert np.array_equal(scales.cpu().numpy(), s64), "scales"
+        assert np.array_equal(X.unpacked(codes.cpu().numpy(), kind), c64), "codes"
+
+
+def test_block_norm_mx_alone_in_place_and_spoilt():
+    gen = torch.Generator().manual_seed(8)
+    M, D = 6, 256
+    r, r64 = rand(gen, M, D)
+    w, w64 = rand(gen, D, mean=1.0, scale=0.1)
+    c = dict(pre="rms", post="none", pre_w=w64, pre_b=None, post_w=None, post_b=None, gate=None, scale=1.0, eps=float(np.float32(1e-5)))
+    same, (codes, scales), none = Q.block_norm_mx(r, pre_weight=w)
+    assert same.data_ptr() == r.data_ptr() and none is None
+    c64, s64 = X.quantize(R.block_norm(r64, None, c)[1].numpy(), "fp8")
+    assert np.array_equal(codes.cpu().numpy(), c64) and np.array_equal(scales.cpu().numpy(), s64)
+    y, y64 = rand(gen, M, D)
+    want, n1, _ = Q.block_norm_mx(r, y, pre_weight=w)
+    y[2, 7], y[4, 9] = math.inf, math.nan
+    got, n2, _ = Q.block_norm_mx(r, y, pre_weight=w, r_out=r)
+    assert got.data_ptr() == r.data_ptr()
+    fine = [0, 1, 3, 5]
+    assert torch.equal(got[fine], want[fine]) and all(torch.equal(a[fine], b[fine]) for a, b in zip(n1, n2))
+    assert (n2[1][4] == 255).all() and n2[1][2, 0] == 255
+    assert Q.block_norm_mx(r[:0], y[:0], pre_weight=w)[1][0].shape == (0, D)
+    # the gradient of the values before the codes is block_norm_backward's
+    r2, (q, s), st = Q.block_norm_mx(want, y.nan_to_num(0, 0, 0), pre_weight=w, save_stats=True)
+    dn, _ = rand(gen, M, D)
+    g = Q.block_norm_backward(r2, y.nan_to_num(0, 0, 0), st, dn, pre_weight=w)
+    f, _, st2 = Q.block_norm(want, y.nan_to_num(0, 0, 0), pre_weight=w, save_stats=True)
+    g2 = Q.block_norm_backward(f, y.nan_to_num(0, 0, 0), st2, dn, pre_weight=w)
+    near(g["dr"], g2["dr"].cpu().double(), 2 * U[torch.bfloat16], "dr")
+
+
+# ---- ends of the range, spoilt values -------------------------------------------------
+
+@pytest.mark.parametrize("x", XS)
+@pytest.mark.parametrize("M", [1, 3, 12, 40, 100])
+def test_spoilt_rows_and_columns_stay_alone(x, M):
+    gen = torch.Generator().manual_seed(M)
+    N, K = 100, 352
+    dt = DT.get(x, torch.bfloat16)
+    w, _ = weight(N, K, 2)
+    xq, _ = activation(gen, M, K, x)
+    clean = Q.mx_linear(w, xq, dtype=dt)
+    bad_w = (w[0], w[1].clone())
+    bad_w[1][7, 3], bad_w[1][99, 10] = 255, 255
+    if x in DT:
+        bad_x = xq.clone()
+        bad_x[M // 2, 17] = math.nan
+    else:
+        bad_x = (xq[0].clone(), xq[1].clone())
+        bad_x[1][M // 2, 4] = 255
+    y = Q.mx_linear(bad_w, bad_x, dtype=dt)
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[M // 2], want[:, 7], want[:, 99] = True, True, True
+    assert torch.equal(torch.isnan(y.cpu()), want)
+    assert torch.equal(y.cpu()[~want], clean.cpu()[~want])
+    if x == "fp8":
+        bad_x[1][M // 2, 4], bad_x[0][M // 2, 351] = 127, 0xFF
+        assert torch.isnan(Q.mx_linear(w, bad_x, dtype=dt)[M // 2]).all()
+    if x in DT:                                                              # an infinity gives what its terms give
+        bad_x = xq.clone()
+        bad_x[M // 2, 5] = math.inf
+        got = Q.mx_linear(w, bad_x, dtype=dt)[M // 2].cpu()
+        col = Q.mx_dequantize(w, dtype=torch.float32)[:, 5].cpu()
+        assert torch.equal(torch.isnan(got), col == 0) and (got[col > 0] == math.inf).all() and (got[col < 0] == -math.inf).all()
+
+
+@pytest.mark.parametrize("x", ["fp8", "fp4"])
+@pytest.mark.parametrize("M", [1, 4, 30, 90])
+def test_scales_over_their_range(x, M):
+    """Blocks of very different scales, and scales whose product only is of ordinary size."""
+    N, K = 48, 288
+    rng = np.random.default_rng(M)
+    for ws, xs in ((1, 250), (250, 1), (0, 254), (60, 190)):
+        cw, cx = rng.integers(0, 16, (N, K)).astype(np.uint8), rng.integers(0, 16 if x == "fp4" else 120, (M, K)).astype(np.uint8)
+        sw, sx = np.full((N, K // 32), ws, np.uint8), np.full((M, K // 32), xs, np.uint8)
+        sw[::2, 1] = 200 if ws < 100 else 20               # against x's scale of the same block
+        sx[:, 1] = 30 if ws < 100 else 210
+        w = (torch.from_numpy(X.planes(cw, "fp4")).cuda(), torch.from_numpy(sw).cuda())
+        xq = (torch.from_numpy(X.planes(cx, x)).cuda(), torch.from_numpy(sx).cuda())
+        # block by block: among a far larger block's terms, which may cancel, binary64 too would lose the others
+        a, b = X.values(cx, sx, x).reshape(M, -1, 32), X.values(cw, sw, "fp4").reshape(N, -1, 32)
+        want = torch.from_numpy(np.matmul(a.transpose(1, 0, 2), b.transpose(1, 2, 0)).sum(0))
+        near(Q.mx_linear(w, xq), want, bar(torch.bfloat16, x), f"scales {ws} {xs}")
+
+
+# ---- streams, graphs, chains ------------------------------------------------------------
+
+@pytest.mark.parametrize("x", XS)
+@pytest.mark.parametrize("M", [1, 8, 50, 200])
+def test_captured_and_on_another_stream(x, M):
+    gen = torch.Generator().manual_seed(M)
+    dt = DT.get(x, torch.bfloat16)
+    w, _ = weight(96, 8192, 1)
+    u, _ = weight(96, 8192, 2)
+    xs = [activation(gen, M, 8192, x, seed=s)[0] for s in (1, 2, 3)]
+    put = (lambda a, b: a.copy_(b)) if x in DT else (lambda a, b: [p.copy_(q) for p, q in zip(a, b)])
+    live = xs[0].clone() if x in DT else tuple(t.clone() for t in xs[0])
+    f = lambda v: (Q.mx_linear(w, v, dtype=dt, act=ACTS["silu"]), Q.mx_gated(w, u, v, dtype=dt))  # noqa: E731
+    want = [f(v) for v in xs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        there = f(xs[1])
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(there, want[1]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f(live)
+    for k in (1, 2, 0, 1):
+        put(live, xs[k])
+        graph.replay()
+        f(xs[(k + 1) % 3])                                                   # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[k])), k
+
+
+@pytest.mark.parametrize("M", [1, 6, 150])
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+def test_feed_forward_half_of_a_layer(M, kind):
+    """norm, gated product, quantisation of h, down projection onto the stream, and the gradients back."""
+    gen = torch.Generator().manual_seed(M)
+    D, F = 256, 544
+    g, G = weight(F, D, 1, 0.06)
+    u, Uw = weight(F, D, 2, 0.06)
+    d, Dw = weight(D, F, 3, 0.06)
+    r, r64 = rand(gen, M, D)
+    y, y64 = rand(gen, M, D)
+    nw, nw64 = rand(gen, D, mean=1.0, scale=0.1)
+    r1, n, st = Q.block_norm_mx(r, y, pre_weight=nw, n_type=TYPES[kind], save_stats=True)
+    h, gp, up = Q.mx_gated(g, u, n, save_pre=True)
+    hq = Q.mx_quantize(h, TYPES[kind])
+    out = Q.mx_linear(d, hq, residual=r1)
+    # each step from what the one before it gave
+    c = dict(pre="rms", post="none", pre_w=nw64, pre_b=None, post_w=None, post_b=None, gate=None, scale=1.0, eps=float(np.float32(1e-5)))
+    n64 = X.values(*X.quantize(R.block_norm(r64, y64, c)[1].numpy(), kind), kind)
+    h64, g64, u64 = R.gated(torch.from_numpy(n64), G, Uw, None, None, "silu")
+    near(gp, g64, bar(torch.bfloat16, kind), "gate")
+    near(h, h64, U[torch.bfloat16] + 4 * (bar(torch.bfloat16, kind) - U[torch.bfloat16]), "h")
+    hq64 = torch.from_numpy(X.values(*X.quantize(h.cpu().double().numpy(), kind), kind))
+    near(out, hq64 @ Dw.T + r1.cpu().double(), bar(torch.bfloat16, kind), "out")
+    dout, dout64 = rand(gen, M, D, scale=0.1)
+    dh = Q.mx_linear_backward(d, dout)["dx"]
+    gg = Q.mx_gated_backward(g, u, dh, gp, up)
+    b = Q.block_norm_backward(r1, y, st, gg["dx"], dout, pre_weight=nw)
+    dh64 = dout64 @ Dw
+    near(dh, dh64, bar(torch.bfloat16), "dh")
+    dx64 = R.gated_grad(G, Uw, dh.cpu().double(), gp.cpu().double(), up.cpu().double(), "silu")[0]
+    near(gg["dx"], dx64, bar(torch.bfloat16), "dx")
+    assert b["dr"].shape == (M, D) and torch.isfinite(b["dr"]).all() and torch.isfinite(b["pre_dw"]).all()
