@@ -1,6 +1,5 @@
 // mx_linear.hip -- mx_linear and mx_gated: which kernels a call takes.
-#include "mx_common.hpp"
-#include "tile_image.hpp"
+#include "mx_tile.hpp"
 
 namespace q4 {
 
@@ -51,15 +50,33 @@ __global__ __launch_bounds__(256) void k_mx_plain(const MxLinearArgs p) {
 
 constexpr int64_t kFewMaxM = 64;
 
+bool is_mx(int x_type) { return x_type == XT_MXFP4 || x_type == XT_MXFP8; }
+
+EpilogueArgs epilogue_args(const LinearArgs& a) {
+    EpilogueArgs e{};
+    e.act = a.act;
+    e.dtype = a.dtype;
+    e.M = a.M;
+    e.N = a.N;
+    for (int i = 0; i < 2; i++) {
+        e.bias[i] = a.bias[i];
+        e.pre[i] = a.pre[i];
+    }
+    e.residual = a.residual;
+    e.y = a.y;
+    return e;
+}
+
 }  // namespace
 
 int64_t mx_linear_workspace_bytes(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
-    if ((x_type == DT_BF16 || x_type == DT_F16) && M > kFewMaxM) return linear_workspace_bytes(WF_MXFP4, nmat, x_type, M, N, K);
-    return 0;
+    if (M <= kFewMaxM) return 0;
+    return is_mx(x_type) ? mx_tile_workspace_bytes(x_type, nmat, M, N, K) : linear_workspace_bytes(WF_MXFP4, nmat, x_type, M, N, K);
 }
 
 hipError_t launch_mx_linear(const MxLinearArgs& p, void* workspace, hipStream_t s) {
-    if ((p.x_type == DT_BF16 || p.x_type == DT_F16) && p.a.M > kFewMaxM) return launch_linear(p.a, workspace, s);
+    if (p.a.M > kFewMaxM)
+        return is_mx(p.x_type) ? launch_mx_tile(p, epilogue_args(p.a), workspace, s) : launch_linear(p.a, workspace, s);
     const int64_t blocks = (p.a.M * p.a.N + 255) / 256;
     if (!launchable(blocks, 256)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(k_mx_plain, dim3((unsigned)blocks), dim3(256), 0, s, p);

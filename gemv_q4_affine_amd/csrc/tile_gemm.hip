@@ -27,10 +27,7 @@
 // GHz; this kernel 1.37 at K = 12288, M = 4096, N = 4096 (300 us, clock 1.67
 // GHz, matrix pipe 0.77 busy).  Without the copies it takes 266 us, without the
 // barriers 299.
-//
-// The epilogue passes the accumulators through LDS, 32 rows at a time, so that
-// bias, residual and outputs move as whole rows of 16 bytes a lane.
-#include "tile_image.hpp"
+#include "tile_epilogue.hpp"
 
 namespace q4 {
 
@@ -42,7 +39,7 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     constexpr int kPanels = 2 * (NT + MT);                  // of a slot: weights first
     constexpr int kSlot = kPanels * 2 * kUnit;              // [panel][slice][unit]
     constexpr int kCopies = NT + MT;                        // of a wave and step
-    constexpr int kRowF = NT * 32 + 4;                      // a row of the epilogue's LDS tile, floats
+    constexpr int kRowF = tile_row_floats<NT>();
     constexpr int kLds = kRing * kSlot > 4 * 32 * kRowF * 4 ? kRing * kSlot : 4 * 32 * kRowF * 4;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
@@ -171,63 +168,9 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     // ---- epilogue ----------------------------------------------------------------
     // every copy has landed and every wave has read its last fragments
     step_barrier<0>();
-    float* tile = reinterpret_cast<float*>(lds) + wave * 32 * kRowF;
-    constexpr int kCols = EPI == EPI_GATED ? NT * 16 : NT * 32;      // output columns of the wave
-    constexpr int kChunks = kCols / 8;
-    const int64_t N = a.epi.N, M = a.epi.M;
-    const int64_t n0 = EPI == EPI_GATED ? (pn0 + wn * NT) * 16 : (pn0 + wn * NT) * 32;
-    const bool vec = N % 8 == 0;
-#pragma unroll
-    for (int j = 0; j < MT; j++) {
-        const int64_t m0 = (pm0 + wm * MT + j) * 32;
-        const int64_t mine = m0 + (lane & 31);
-        // (parts of a sum are joined first: alone they may leave the range)
-        const float back = EPI == EPI_PARTIAL ? 1.0f : mine < M ? ldexpf(1.0f, -(int)a.xexp[mine]) : 0.0f;
-        // lane: row lane & 31 of the panel, columns 8 (e / 4) + 4 (lane >> 5) + e % 4
-#pragma unroll
-        for (int i = 0; i < NT; i++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                floatx4_t t;
-#pragma unroll
-                for (int e = 0; e < 4; e++) t[e] = acc[i][j][4 * q + e] * back;
-                *reinterpret_cast<floatx4_t*>(tile + (lane & 31) * kRowF + i * 32 + 8 * q + 4 * (lane >> 5)) = t;
-            }
-        for (int c0 = 0; c0 < 32 * kChunks; c0 += 64) {
-            const int c = c0 + lane;
-            const int row = c / kChunks, col = c % kChunks * 8;
-            const int64_t m = m0 + row, n = n0 + col;
-            float z[8], z2[8];
-            auto fetch = [&](int at, float (&f)[8]) __attribute__((always_inline)) {
-                const floatx4_t* p = reinterpret_cast<const floatx4_t*>(tile + row * kRowF + at);
-                const floatx4_t lo = p[0], hi = p[1];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    f[e] = lo[e];
-                    f[4 + e] = hi[e];
-                }
-            };
-            if constexpr (EPI == EPI_GATED) {
-                fetch(col / 32 * 64 + col % 32, z);
-                fetch(col / 32 * 64 + 32 + col % 32, z2);
-            } else {
-                fetch(col, z);
-            }
-            if (m >= M) continue;
-            if constexpr (EPI == EPI_PARTIAL) {
-                const int64_t np = a.w_panels * 32;
-                if (n < np) {
-                    floatx4_t* p = reinterpret_cast<floatx4_t*>(a.part + ((int64_t)part * M + m) * np + n);
-                    p[0] = floatx4_t{z[0], z[1], z[2], z[3]};
-                    p[1] = floatx4_t{z[4], z[5], z[6], z[7]};
-                }
-            } else {
-                if (n >= N) continue;
-                if (vec) epilogue8<EPI, true>(a.epi, m, n, z, z2);
-                else epilogue8<EPI, false>(a.epi, m, n, z, z2);
-            }
-        }
-    }
+    tile_epilogue<NT, MT, EPI>(acc, reinterpret_cast<float*>(lds) + wave * 32 * kRowF, a.epi, a.part, part, a.w_panels,
+                               EPI == EPI_GATED ? (pn0 + wn * NT) * 16 : (pn0 + wn * NT) * 32, (pm0 + wm * MT) * 32,
+                               [&](int64_t m) __attribute__((always_inline)) { return ldexpf(1.0f, -(int)a.xexp[m]); });
 }
 
 // The parts of a split sum joined in order and scaled, then the epilogue: one

@@ -80,6 +80,7 @@ int mx_dequantize(int type, const uint8_t* codes, const uint8_t* scales, void* v
  * With 16-bit x above 64 rows, and in the gradients, W must fit binary16 and x
  * (dz) is scaled per row by a power of two, as in q4_linear.
  *
+ * (The terms of a sum have to stay in binary32's range, 3.4e38.)
  * A row of x with an infinity or a NaN (a NaN code or scale) spoils no other
  * row of y, and a column of W with a NaN scale no other column.
  */

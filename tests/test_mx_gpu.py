@@ -404,7 +404,11 @@ def test_scales_over_their_range(x, M):
         # block by block: among a far larger block's terms, which may cancel, binary64 too would lose the others
         a, b = X.values(cx, sx, x).reshape(M, -1, 32), X.values(cw, sw, "fp4").reshape(N, -1, 32)
         want = torch.from_numpy(np.matmul(a.transpose(1, 0, 2), b.transpose(1, 2, 0)).sum(0))
-        near(Q.mx_linear(w, xq), want, bar(torch.bfloat16, x), f"scales {ws} {xs}")
+        got = Q.mx_linear(w, xq).cpu()
+        # 2^206 and more in a block of some columns: terms past binary32's range, where a sum is nothing that it says
+        past = torch.from_numpy(((np.abs(a[:, None]) * np.abs(b[None])).max((2, 3)) >= 2.0 ** 127))
+        assert not torch.isfinite(got[want.abs() > 2.0 ** 128]).any()
+        near(got[~past], want[~past], bar(torch.bfloat16, x), f"scales {ws} {xs}")
 
 
 # ---- streams, graphs, chains ------------------------------------------------------------
