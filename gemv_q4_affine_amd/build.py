@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libq4.so")
 SOURCES = ["quant.hip", "gemv.hip", "gemm.hip", "gemm_big.hip", "gemm_q8.hip", "affine8.hip", "noalloc.hip",
            "capi.cpp", "block_capi.cpp", "linear.hip", "linear_few_q4_0.hip", "linear_few_affine4.hip",
            "linear_few_affine8.hip", "tile_gemm.hip", "tile_pack.hip", "norm.hip", "mx_capi.cpp", "mx_quant.hip",
-           "mx_norm.hip", "mx_linear.hip", "mx_tile.hip"]
+           "mx_norm.hip", "mx_linear.hip", "mx_tile.hip", "mx_few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

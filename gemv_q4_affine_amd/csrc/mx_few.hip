@@ -1,0 +1,313 @@
+// mx_few.hip -- mx_linear and mx_gated at few rows (decode, small batches): the
+// weights are streamed once, straight from their planes into the matrix
+// instruction's registers.
+//
+// Mathematics.  With MX x a 16x16x128 scaled MFMA takes the codes and scales as
+// they are.  With 16-bit x the codes are converted with their scale to bfloat16,
+// which holds them exactly (2 bits and any scale), and multiplied by bfloat16 x
+// in four 16x16x32 MFMAs; binary16 x is split into two bfloat16 parts, x = hi + lo
+// exactly, and takes eight.  Products are exact, sums binary32.
+//
+// Layout.  Lane l of the MFMA holds one block of 32 of A's row j = l & 15, block
+// slot g = l >> 4.  Taken as 16 rows of W, neighbouring lanes lie on different rows.
+// Up to four rows of x (P = 4) A's row j is instead slice p = j & 3 of row j >> 2
+// of W, and B's column the slice q = c & 3 of row c >> 2 of x: a load of W is four
+// rows by 256 contiguous bytes, and of the 16 x 16 sums those with p = q count,
+// four lanes' worth added up at the end.  Above four rows P is 1.
+//
+// A wave takes groups of four such chunks, 64 P^-1 .. k, of R row tiles; the waves of a
+// workgroup split the sum (KW of them) and the rows, and add their sums through
+// LDS in wave order.  Scales: one 16-byte load a tile and group.
+#include "mx_few.hpp"
+
+namespace q4 {
+
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef u32x4_t u32x4_b __attribute__((aligned(1)));
+
+// Dword r of lane row g's 16 bytes -> dword g of lane row r's.
+__device__ __forceinline__ void transpose4(u32x4_t& q) {
+    uint32_t a = q[0], b = q[1], c = q[2], d = q[3];
+    auto swap32 = [](uint32_t& x, uint32_t& y) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+    };
+    auto swap16 = [](uint32_t& x, uint32_t& y) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        x = r[0];
+        y = r[1];
+    };
+    swap32(a, c);
+    swap32(b, d);
+    swap16(a, b);
+    swap16(c, d);
+    q = u32x4_t{a, b, c, d};
+}
+
+// Sixteen scales of a row from block `first` on, zeros past the row's nb.
+__device__ __forceinline__ u32x4_t scales16(const uint8_t* row, int first, int nb) {
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (first + 16 <= nb) return *reinterpret_cast<const u32x4_b*>(row + first);
+#pragma unroll
+    for (int e = 0; e < 16; e++)
+        if (first + e < nb) v[e >> 2] |= (uint32_t)row[first + e] << (8 * (e & 3));
+    return v;
+}
+
+}  // namespace
+
+template <int XT, int P, int MT, int NM, int R>
+__global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, const MxFewPlan plan) {
+    static_assert(P == 1 || MT == 1, "slices for few rows");
+    constexpr bool kMx = XT == XT_MXFP4 || XT == XT_MXFP8;
+    constexpr int kRows = 16 / P;                            // rows of W of a tile
+    constexpr int kTile = P == 4 ? 16 : 256 * MT;            // sums of a tile: [row][x row]
+    constexpr int kGroup = 16 * P;                           // blocks of a group of four chunks
+    __shared__ float red[8 * R * NM * kTile];
+    const LinearArgs& a = args.a;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kw = wave % plan.kw, rw = wave / plan.kw;
+    const int j = lane & 15, g = lane >> 4, p = j & (P - 1);
+    const int K = (int)a.K, N = (int)a.N, M = (int)a.M, nb = K / 32;
+    const int n_first = ((int)blockIdx.x * plan.rw + rw) * R * kRows;
+
+    const uint8_t* wq[R][NM];
+    const uint8_t* wsc[R][NM];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int t = 0; t < NM; t++) {
+            int n = n_first + r * kRows + j / P;             // rows past N repeat the last one (never stored)
+            n = n < N ? n : N - 1;
+            wq[r][t] = a.w[t].q + (int64_t)n * (K / 2);
+            wsc[r][t] = reinterpret_cast<const uint8_t*>(a.w[t].s) + (int64_t)n * nb;
+        }
+    int xm[MT];                                              // this lane's rows of x
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+        xm[i] = i * 16 + j / P;
+        xm[i] = xm[i] < M ? xm[i] : M - 1;
+    }
+
+    floatx4_t acc[R][NM][MT];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int t = 0; t < NM; t++)
+#pragma unroll
+            for (int i = 0; i < MT; i++) acc[r][t][i] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int groups = (nb + kGroup - 1) / kGroup;
+    for (int kg = kw; kg < groups; kg += plan.kw) {
+        const int b0 = kg * kGroup;
+        // this lane's block of chunk c, kept inside the row
+        auto block = [&](int c, int slot) __attribute__((always_inline)) {
+            const int b = b0 + c * 4 * P + slot * P + p;
+            return b < nb ? b : nb - 1;
+        };
+        u32x4_t w[R][NM][4], ws[R][NM];
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int t = 0; t < NM; t++) {
+#pragma unroll
+                for (int c = 0; c < 4; c++) w[r][t][c] = *reinterpret_cast<const u32x4_t*>(wq[r][t] + (int64_t)block(c, g) * 16);
+                ws[r][t] = scales16(wsc[r][t], b0 + (P == 4 ? 16 * g : 0), nb);
+            }
+        // dword c: the scale of this lane's block of chunk c, in byte 0
+        auto place = [&](u32x4_t& s) __attribute__((always_inline)) {
+            if constexpr (P == 4) transpose4(s);
+#pragma unroll
+            for (int c = 0; c < 4; c++) s[c] >>= 8 * (P == 4 ? p : g);
+        };
+        u32x4_t xs[MT];
+        if constexpr (kMx) {
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                xs[i] = scales16(args.x_s + (int64_t)xm[i] * nb, b0 + (P == 4 ? 16 * g : 0), nb);
+                place(xs[i]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int t = 0; t < NM; t++) place(ws[r][t]);
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            if constexpr (kMx) {
+                i32x8_t x[MT];
+#pragma unroll
+                for (int i = 0; i < MT; i++) {
+                    const uint8_t* row = static_cast<const uint8_t*>(a.x) + (int64_t)xm[i] * (XT == XT_MXFP8 ? K : K / 2);
+                    x[i] = i32x8_t{};
+                    u32x4_t lo, hi = {0u, 0u, 0u, 0u};
+                    if constexpr (XT == XT_MXFP8) {
+                        // the instruction's 8-bit order: half g & 1 of slots g >> 1 and 2 + (g >> 1)
+                        lo = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, g >> 1) * 32 + 16 * (g & 1));
+                        hi = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, 2 + (g >> 1)) * 32 + 16 * (g & 1));
+                    } else {
+                        lo = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, g) * 16);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        x[i][e] = (int)lo[e];
+                        if constexpr (XT == XT_MXFP8) x[i][4 + e] = (int)hi[e];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; r++)
+#pragma unroll
+                    for (int t = 0; t < NM; t++) {
+                        i32x8_t v = {};
+#pragma unroll
+                        for (int e = 0; e < 4; e++) v[e] = (int)w[r][t][c][e];
+#pragma unroll
+                        for (int i = 0; i < MT; i++)
+                            acc[r][t][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                v, x[i], acc[r][t][i], 4, XT == XT_MXFP8 ? 0 : 4, 0, (int)ws[r][t][c], 0, (int)xs[i][c]);
+                    }
+            } else {
+                const bool in = b0 + c * 4 * P + g * P + p < nb;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {                // elements 8 e .. + 7 of every block
+                    u32x4_t hi[MT], lo[MT];
+#pragma unroll
+                    for (int i = 0; i < MT; i++) {
+                        const uint16_t* row = static_cast<const uint16_t*>(a.x) + (int64_t)xm[i] * K;
+                        u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, g) * 32 + 8 * e);
+                        if (!in) v = u32x4_t{0u, 0u, 0u, 0u};
+                        if constexpr (XT == DT_BF16) {
+                            hi[i] = v;
+                        } else {
+                            split_f16(v, hi[i], lo[i]);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; r++)
+#pragma unroll
+                        for (int t = 0; t < NM; t++) {
+                            const float s = mx_scale(ws[r][t][c] & 0xFFu);
+                            const uint32_t d = w[r][t][c][e];
+                            const u32x4_t q = {bf16_pair<0>(d, s), bf16_pair<1>(d, s), bf16_pair<2>(d, s), bf16_pair<3>(d, s)};
+#pragma unroll
+                            for (int i = 0; i < MT; i++) {
+                                acc[r][t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    __builtin_bit_cast(bf16x8_t, q), __builtin_bit_cast(bf16x8_t, hi[i]), acc[r][t][i], 0, 0, 0);
+                                if constexpr (XT == DT_F16)
+                                    acc[r][t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                        __builtin_bit_cast(bf16x8_t, q), __builtin_bit_cast(bf16x8_t, lo[i]), acc[r][t][i], 0, 0, 0);
+                            }
+                        }
+                }
+            }
+        }
+    }
+
+    // ---- the waves' sums, joined in order ----
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int t = 0; t < NM; t++) {
+            float* to = red + ((wave * R + r) * NM + t) * kTile;
+            if constexpr (P == 4) {
+                // lane (column c = 4 m + q, row g of W): its slice's sum, added over the four slices
+                const floatx4_t v = acc[r][t][0];
+                float s = p == 0 ? v[0] : p == 1 ? v[1] : p == 2 ? v[2] : v[3];
+                s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0xB1, 0xF, 0xF, false));
+                s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x4E, 0xF, 0xF, false));
+                if (p == 0) to[g * 4 + (j >> 2)] = s;
+            } else {
+#pragma unroll
+                for (int i = 0; i < MT; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) to[(4 * g + e) * 16 * MT + i * 16 + j] = acc[r][t][i][e];
+            }
+        }
+    __syncthreads();
+    constexpr int kWide = P == 4 ? 4 : 16 * MT;              // x rows of a tile's sums
+    const int outputs = plan.rw * R * kRows * M, n0 = (int)blockIdx.x * plan.rw * R * kRows;
+    for (int o = threadIdx.x; o < outputs; o += blockDim.x) {
+        const int m = o / (plan.rw * R * kRows), i = o % (plan.rw * R * kRows), n = n0 + i;
+        if (n >= N) continue;
+        const int tile = i / kRows, from = tile / R;          // row tile of the workgroup, its wave row
+        auto sum = [&](int t) __attribute__((always_inline)) {
+            float z = 0.0f;
+            for (int k = 0; k < plan.kw; k++)
+                z += red[(((from * plan.kw + k) * R + tile % R) * NM + t) * kTile + (i % kRows) * kWide + m];
+            return z;
+        };
+        const int64_t at = (int64_t)m * N + n;
+        float z = sum(0);
+        if (a.bias[0]) z += load_elem(a.bias[0], a.dtype, n);
+        if (a.pre[0]) store_elem(a.pre[0], a.dtype, at, z);
+        float zs[1] = {z}, none[1];
+        activate_all<false>(a.act, zs, zs, none);
+        float y = zs[0];
+        if constexpr (NM == 2) {
+            float u = sum(1);
+            if (a.bias[1]) u += load_elem(a.bias[1], a.dtype, n);
+            if (a.pre[1]) store_elem(a.pre[1], a.dtype, at, u);
+            y *= u;
+        }
+        if (a.residual) y += load_elem(a.residual, a.dtype, at);
+        store_elem(a.y, a.dtype, at, y);
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+namespace {
+
+MxFewPlan plan_few(int64_t M, int64_t N, int64_t K) {
+    const int P = M <= 4 ? 4 : 1;
+    const int64_t groups = (K / 32 + 16 * P - 1) / (16 * P), tiles = (N + 16 / P - 1) / (16 / P);
+    MxFewPlan p{};
+    p.kw = (int)(groups < 8 ? groups : 8);
+    p.rw = 8 / p.kw;
+    const int64_t per = tiles / ((int64_t)p.rw * current_cu_count());
+    p.r = per <= 1 ? 1 : per == 2 ? 2 : 3;
+    return p;
+}
+
+template <int XT, int P, int MT, int NM, int R>
+void launch(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
+    const int64_t cols = (int64_t)p.rw * R * (16 / P);
+    hipLaunchKernelGGL((k_mx_few<XT, P, MT, NM, R>), dim3((unsigned)((a.a.N + cols - 1) / cols)), dim3(64 * p.kw * p.rw), 0, s, a, p);
+}
+template <int XT, int P, int MT, int NM>
+void launch_r(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
+    if constexpr (P == 4 || MT * NM < 8) {
+        if (p.r == 2) return launch<XT, P, MT, NM, 2>(a, p, s);
+        if (p.r == 3) return launch<XT, P, MT, NM, 3>(a, p, s);
+    }
+    launch<XT, P, MT, NM, 1>(a, p, s);
+}
+template <int XT, int NM>
+void launch_m(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
+    if (a.a.M <= 4) launch_r<XT, 4, 1, NM>(a, p, s);
+    else if (a.a.M <= 16) launch_r<XT, 1, 1, NM>(a, p, s);
+    else if (a.a.M <= 32) launch_r<XT, 1, 2, NM>(a, p, s);
+    else launch_r<XT, 1, 4, NM>(a, p, s);
+}
+template <int XT>
+void launch_x(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
+    if (a.a.nmat == 2) launch_m<XT, 2>(a, p, s);
+    else launch_m<XT, 1>(a, p, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx_few(const MxLinearArgs& a, hipStream_t s) {
+    const MxFewPlan p = plan_few(a.a.M, a.a.N, a.a.K);
+    if (a.x_type == XT_MXFP8) launch_x<XT_MXFP8>(a, p, s);
+    else if (a.x_type == XT_MXFP4) launch_x<XT_MXFP4>(a, p, s);
+    else if (a.x_type == DT_BF16) launch_x<DT_BF16>(a, p, s);
+    else launch_x<DT_F16>(a, p, s);
+    return hipGetLastError();
+}
+
+}  // namespace q4
