@@ -18,7 +18,9 @@
 // A wave takes groups of four such chunks, 64 P^-1 .. k, of R row tiles; the waves of a
 // workgroup split the sum (KW of them) and the rows, and add their sums through
 // LDS in wave order.  Scales: one 16-byte load a tile and group.
+#include "gemm_common.hpp"
 #include "mx_few.hpp"
+#include "tile_image.hpp"
 
 namespace q4 {
 
@@ -58,6 +60,33 @@ __device__ __forceinline__ u32x4_t scales16(const uint8_t* row, int first, int n
     return v;
 }
 
+// Four consecutive 16-bit values, `left` of them inside the tensor; vec: rows
+// are multiples of four.
+__device__ __forceinline__ void add4(const void* p, int dt, int64_t at, int left, bool vec, float (&z)[4]) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    if (vec) {
+        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(q);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint32_t h = (v[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+            z[e] += dt == DT_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        if (e < left) z[e] += load_elem(p, dt, at + e);
+}
+__device__ __forceinline__ void put4(void* p, int dt, int64_t at, int left, bool vec, const float (&z)[4]) {
+    if (vec) {
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p) + at) = u32x2_t{pack2(dt, z[0], z[1]), pack2(dt, z[2], z[3])};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        if (e < left) store_elem(p, dt, at + e, z[e]);
+}
+
 }  // namespace
 
 template <int XT, int P, int MT, int NM, int R>
@@ -65,9 +94,15 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
     static_assert(P == 1 || MT == 1, "slices for few rows");
     constexpr bool kMx = XT == XT_MXFP4 || XT == XT_MXFP8;
     constexpr int kRows = 16 / P;                            // rows of W of a tile
-    constexpr int kTile = P == 4 ? 16 : 256 * MT;            // sums of a tile: [row][x row]
+    constexpr int kPitch = P == 4 ? 4 : 20;                  // sums of a tile: [x row][row of W], rows spread over the banks
+    constexpr int kTile = (P == 4 ? 4 : 16 * MT) * kPitch;
     constexpr int kGroup = 16 * P;                           // blocks of a group of four chunks
-    __shared__ float red[8 * R * NM * kTile];
+    // x of a wave's stage of kStage chunks (P = 1): [chunk][tile of 16 rows][row][kRowB]
+    constexpr int kRowB = XT == XT_MXFP8 ? 128 : XT == XT_MXFP4 ? 64 : 256;
+    constexpr int kFit = 16384 / (kRowB * 16 * MT), kStage = P == 4 ? 0 : kFit < 4 ? kFit : 4;
+    constexpr int kStageB = kStage * MT * 16 * kRowB, kRed = 8 * R * NM * kTile * 4;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[8 * kStageB > kRed ? 8 * kStageB : kRed];
+    float* red = reinterpret_cast<float*>(lds);
     const LinearArgs& a = args.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kw = wave % plan.kw, rw = wave / plan.kw;
@@ -100,6 +135,35 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
         for (int t = 0; t < NM; t++)
 #pragma unroll
             for (int i = 0; i < MT; i++) acc[r][t][i] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // ---- P = 1: x by direct copies of whole lines, the pieces of 16 bytes of a row
+    // placed by an XOR with the row, so that a wave's reads meet no bank twice ----
+    constexpr int kPieces = kRowB / 16, kCopyRows = 64 / kPieces;       // of a row; rows of a copy
+    auto swz = [](int r) { return kPieces == 4 ? ((r >> 1) & 3) ^ ((r >> 3) & 1) : kPieces == 8 ? (r & 7) ^ ((r >> 3) & 1) : r; };
+    const uint32_t row_x = (uint32_t)(kMx ? (XT == XT_MXFP8 ? K : K / 2) : 2 * K), last_x = row_x / 16 - 1;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds) +
+                          (uint32_t)(wave * kStageB);
+    auto stage_x = [&](int b0) __attribute__((always_inline)) {         // from block b0 on
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+            const int first = i * 16 < M ? i * 16 : M - 1;
+            const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)first * row_x;
+#pragma unroll
+            for (int h = 0; h < 16 / kCopyRows; h++) {
+                const int r = h * kCopyRows + lane / kPieces, in = M - 1 - first;
+                const uint32_t at = (uint32_t)(r < in ? r : in) * row_x;
+#pragma unroll
+                for (int c = 0; c < kStage; c++) {
+                    const uint32_t piece = (uint32_t)(b0 / 4 + c) * kPieces + (uint32_t)((lane % kPieces) ^ swz(r));
+                    copy_unit(src, at + (piece < last_x ? piece : last_x) * 16,
+                              lds0 + (uint32_t)(((c * MT + i) * 16 + h * kCopyRows) * kRowB));
+                }
+            }
+        }
+    };
+    auto staged = [&](int c, int i, int piece) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4_t*>(lds + wave * kStageB + ((c * MT + i) * 16 + j) * kRowB + ((piece ^ swz(j)) * 16));
+    };
 
     const int groups = (nb + kGroup - 1) / kGroup;
     for (int kg = kw; kg < groups; kg += plan.kw) {
@@ -138,6 +202,16 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
             for (int t = 0; t < NM; t++) place(ws[r][t]);
 #pragma unroll
         for (int c = 0; c < 4; c++) {
+            if constexpr (P == 1) {
+                if (c % kStage == 0) {
+                    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                    __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0): the stage before is read
+                    stage_x(b0 + 4 * c);
+                    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                    Q4_WAIT_VMCNT(0);
+                    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                }
+            }
             if constexpr (kMx) {
                 i32x8_t x[MT];
 #pragma unroll
@@ -145,7 +219,10 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
                     const uint8_t* row = static_cast<const uint8_t*>(a.x) + (int64_t)xm[i] * (XT == XT_MXFP8 ? K : K / 2);
                     x[i] = i32x8_t{};
                     u32x4_t lo, hi = {0u, 0u, 0u, 0u};
-                    if constexpr (XT == XT_MXFP8) {
+                    if constexpr (P == 1) {
+                        lo = staged(c % kStage, i, g);
+                        if constexpr (XT == XT_MXFP8) hi = staged(c % kStage, i, 4 + g);
+                    } else if constexpr (XT == XT_MXFP8) {
                         // the instruction's 8-bit order: half g & 1 of slots g >> 1 and 2 + (g >> 1)
                         lo = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, g >> 1) * 32 + 16 * (g & 1));
                         hi = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, 2 + (g >> 1)) * 32 + 16 * (g & 1));
@@ -178,7 +255,9 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
 #pragma unroll
                     for (int i = 0; i < MT; i++) {
                         const uint16_t* row = static_cast<const uint16_t*>(a.x) + (int64_t)xm[i] * K;
-                        u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, g) * 32 + 8 * e);
+                        u32x4_t v;
+                        if constexpr (P == 1) v = staged(c % kStage, i, 4 * g + e);
+                        else v = *reinterpret_cast<const u32x4_t*>(row + (int64_t)block(c, g) * 32 + 8 * e);
                         if (!in) v = u32x4_t{0u, 0u, 0u, 0u};
                         if constexpr (XT == DT_BF16) {
                             hi[i] = v;
@@ -208,6 +287,7 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
     }
 
     // ---- the waves' sums, joined in order ----
+    if constexpr (P == 1) __syncthreads();                   // they lie where x was
 #pragma unroll
     for (int r = 0; r < R; r++)
 #pragma unroll
@@ -219,42 +299,44 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
                 float s = p == 0 ? v[0] : p == 1 ? v[1] : p == 2 ? v[2] : v[3];
                 s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0xB1, 0xF, 0xF, false));
                 s += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(s), 0x4E, 0xF, 0xF, false));
-                if (p == 0) to[g * 4 + (j >> 2)] = s;
+                if (p == 0) to[(j >> 2) * kPitch + g] = s;
             } else {
 #pragma unroll
-                for (int i = 0; i < MT; i++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) to[(4 * g + e) * 16 * MT + i * 16 + j] = acc[r][t][i][e];
+                for (int i = 0; i < MT; i++) *reinterpret_cast<floatx4_t*>(to + (i * 16 + j) * kPitch + 4 * g) = acc[r][t][i];
             }
         }
     __syncthreads();
-    constexpr int kWide = P == 4 ? 4 : 16 * MT;              // x rows of a tile's sums
-    const int outputs = plan.rw * R * kRows * M, n0 = (int)blockIdx.x * plan.rw * R * kRows;
-    for (int o = threadIdx.x; o < outputs; o += blockDim.x) {
-        const int m = o / (plan.rw * R * kRows), i = o % (plan.rw * R * kRows), n = n0 + i;
-        if (n >= N) continue;
+    // four columns a thread
+    const int cols = plan.rw * R * kRows, quads = cols / 4, n0 = (int)blockIdx.x * cols;
+    const bool vec = N % 4 == 0;
+    for (int o = threadIdx.x; o < quads * M; o += blockDim.x) {
+        const int m = o / quads, i = o % quads * 4, n = n0 + i, left = N - n;
+        if (left <= 0) continue;
         const int tile = i / kRows, from = tile / R;          // row tile of the workgroup, its wave row
-        auto sum = [&](int t) __attribute__((always_inline)) {
-            float z = 0.0f;
+        auto sum = [&](int t, float (&z)[4]) __attribute__((always_inline)) {
+            floatx4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
             for (int k = 0; k < plan.kw; k++)
-                z += red[(((from * plan.kw + k) * R + tile % R) * NM + t) * kTile + (i % kRows) * kWide + m];
-            return z;
+                v += *reinterpret_cast<const floatx4_t*>(red + (((from * plan.kw + k) * R + tile % R) * NM + t) * kTile +
+                                                         m * kPitch + i % kRows);
+#pragma unroll
+            for (int e = 0; e < 4; e++) z[e] = v[e];
         };
         const int64_t at = (int64_t)m * N + n;
-        float z = sum(0);
-        if (a.bias[0]) z += load_elem(a.bias[0], a.dtype, n);
-        if (a.pre[0]) store_elem(a.pre[0], a.dtype, at, z);
-        float zs[1] = {z}, none[1];
-        activate_all<false>(a.act, zs, zs, none);
-        float y = zs[0];
+        float z[4], none[4];
+        sum(0, z);
+        if (a.bias[0]) add4(a.bias[0], a.dtype, n, left, vec, z);
+        if (a.pre[0]) put4(a.pre[0], a.dtype, at, left, vec, z);
+        activate_all<false>(a.act, z, z, none);
         if constexpr (NM == 2) {
-            float u = sum(1);
-            if (a.bias[1]) u += load_elem(a.bias[1], a.dtype, n);
-            if (a.pre[1]) store_elem(a.pre[1], a.dtype, at, u);
-            y *= u;
+            float u[4];
+            sum(1, u);
+            if (a.bias[1]) add4(a.bias[1], a.dtype, n, left, vec, u);
+            if (a.pre[1]) put4(a.pre[1], a.dtype, at, left, vec, u);
+#pragma unroll
+            for (int e = 0; e < 4; e++) z[e] *= u[e];
         }
-        if (a.residual) y += load_elem(a.residual, a.dtype, at);
-        store_elem(a.y, a.dtype, at, y);
+        if (a.residual) add4(a.residual, a.dtype, at, left, vec, z);
+        put4(a.y, a.dtype, at, left, vec, z);
     }
 }
 
