@@ -9,7 +9,8 @@
 // odd (cut, with the last bit set where anything was cut off), after which the
 // second rounding gives what one rounding of n would.
 //
-// A workgroup holds a row in registers, V pieces of eight values a thread; four
+// A workgroup holds a row in registers as it lies in memory, V pieces of eight
+// values a thread, and the next row is requested before this row's sums; four
 // lanes share a block of 32.
 #include "mx_common.hpp"
 #include "tile_image.hpp"
@@ -19,25 +20,48 @@ namespace q4 {
 
 namespace {
 
+// Sum over a wave, the same in every lane: DPP inside rows of 16 lanes (swap
+// neighbours, pairs, halves of eight, eights), then the lane swaps between them.
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v) {
+    const u32x2_t b = __builtin_bit_cast(u32x2_t, v);
+    const u32x2_t t = {(uint32_t)__builtin_amdgcn_mov_dpp((int)b[0], CTRL, 0xF, 0xF, false),
+                       (uint32_t)__builtin_amdgcn_mov_dpp((int)b[1], CTRL, 0xF, 0xF, false)};
+    return v + __builtin_bit_cast(double, t);
+}
 __device__ __forceinline__ double lanes_sum(double v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
-    return v;
+    v = dpp_add<0xB1>(v);
+    v = dpp_add<0x4E>(v);
+    v = dpp_add<0x141>(v);
+    v = dpp_add<0x140>(v);
+    u32x2_t b = __builtin_bit_cast(u32x2_t, v);
+    auto lo = __builtin_amdgcn_permlane16_swap(b[0], b[0], false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap(b[1], b[1], false, false);
+    v = __builtin_bit_cast(double, u32x2_t{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2_t{lo[1], hi[1]});
+    b = __builtin_bit_cast(u32x2_t, v);
+    lo = __builtin_amdgcn_permlane32_swap(b[0], b[0], false, false);
+    hi = __builtin_amdgcn_permlane32_swap(b[1], b[1], false, false);
+    return __builtin_bit_cast(double, u32x2_t{lo[0], hi[0]}) + __builtin_bit_cast(double, u32x2_t{lo[1], hi[1]});
 }
 
+// Eight values of a row as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void get8(const void* p, int64_t i, float (&f)[8]) {
-    if constexpr (DT == DT_F32) {
-        const floatx4_t* q = reinterpret_cast<const floatx4_t*>(static_cast<const float*>(p) + i);
-        const floatx4_t lo = q[0], hi = q[1];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            f[e] = lo[e];
-            f[4 + e] = hi[e];
-        }
-    } else {
-        unpack8(DT, load8_raw<true>(p, i, 8), f);
-    }
+struct Raw {
+    u32x4_t v[DT == DT_F32 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw<DT> get8(const void* p, int64_t i) {
+    Raw<DT> r;
+    const u32x4_t* q = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + i * (DT == DT_F32 ? 4 : 2));
+    r.v[0] = q[0];
+    if constexpr (DT == DT_F32) r.v[1] = q[1];
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ float value(const Raw<DT>& r, int e) {
+    if constexpr (DT == DT_F32) return __uint_as_float(r.v[e >> 2][e & 3]);
+    else if constexpr (DT == DT_BF16) return __uint_as_float(e & 1 ? r.v[0][e >> 1] & 0xFFFF0000u : r.v[0][e >> 1] << 16);
+    else return f16_to_f32((r.v[0][e >> 1] >> (16 * (e & 1))) & 0xFFFFu);
 }
 template <int DT>
 __device__ __forceinline__ void put8(void* p, int64_t i, const float (&f)[8]) {
@@ -82,10 +106,17 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
         for (int w = 0; w < waves; w++) s += mine[w];
         return s;
     };
+    // pieces past the row's end read its last one and count for nothing
+    int at[V];
     bool in[V];
 #pragma unroll
-    for (int v = 0; v < V; v++) in[v] = (int64_t)(v * T + tid) * 8 < D;
-    auto stats = [&](const double (&x)[V][8], int kind, double& mean, double& rstd) __attribute__((always_inline)) {
+    for (int v = 0; v < V; v++) {
+        at[v] = (v * T + tid) * 8;
+        in[v] = at[v] < (int)D;
+        if (!in[v]) at[v] = (int)D - 8;
+    }
+    // mean and 1 / sqrt(variance + eps) of x(v, e), by the norm's kind
+    auto stats = [&](auto x, int kind, double& mean, double& rstd) __attribute__((always_inline)) {
         mean = 0.0;
         rstd = 1.0;
         if (kind == NORM_NONE) return;
@@ -93,86 +124,121 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
         if (kind == NORM_LAYER) {
 #pragma unroll
             for (int v = 0; v < V; v++)
+                if (in[v])
 #pragma unroll
-                for (int e = 0; e < 8; e++) s += x[v][e];          // zeros past the row's end
+                    for (int e = 0; e < 8; e++) s += x(v, e);
             mean = row_sum(s) * inv;
             s = 0.0;
         }
 #pragma unroll
         for (int v = 0; v < V; v++)
+            if (in[v])
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const double d = in[v] ? x[v][e] - mean : 0.0;
-                s = fma(d, d, s);
-            }
+                for (int e = 0; e < 8; e++) {
+                    const double d = x(v, e) - mean;
+                    s = fma(d, d, s);
+                }
         rstd = 1.0 / sqrt(fma(row_sum(s), inv, (double)a.eps));
     };
-    // (v - mean) * rstd * w + b of one value
+    Raw<RT> nr[V];
+    Raw<DT> ny[V];
+    auto request = [&](int64_t m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            nr[v] = get8<RT>(a.r, m * D + at[v]);
+            if (a.y) ny[v] = get8<DT>(a.y, m * D + at[v]);
+        }
+    };
+    if (blockIdx.x < a.M) request(blockIdx.x);
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
         const int64_t o = m * D;
         double r[V][8], m0 = 0.0, i0 = 1.0, m1, i1;
+        Raw<DT> y[V];
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (in[v]) get8<RT>(a.r, o + (v * T + tid) * 8, f);
+            y[v] = ny[v];
 #pragma unroll
-            for (int e = 0; e < 8; e++) r[v][e] = (double)f[e];
+            for (int e = 0; e < 8; e++) r[v][e] = (double)value<RT>(nr[v], e);
         }
+        if (m + gridDim.x < a.M) request(m + gridDim.x);
         if (a.y) {
             const int64_t gr = a.gate_rows >= a.M ? 0 : (uint32_t)m / (uint32_t)a.gate_rows;
-            double y[V][8];
+            stats([&](int v, int e) __attribute__((always_inline)) { return (double)value<DT>(y[v], e); }, a.post, m0, i0);
+            const double scale = (double)a.scale;
 #pragma unroll
             for (int v = 0; v < V; v++) {
-                float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (in[v]) get8<DT>(a.y, o + (v * T + tid) * 8, f);
+                // scale gate ((y - mean) rstd w + b)
+                double p[8];
 #pragma unroll
-                for (int e = 0; e < 8; e++) y[v][e] = (double)f[e];
-            }
-            stats(y, a.post, m0, i0);
+                for (int e = 0; e < 8; e++) p[e] = ((double)value<DT>(y[v], e) - m0) * i0;
+                if (a.post_w) {
+                    const Raw<DT> w = get8<DT>(a.post_w, at[v]);
 #pragma unroll
-            for (int v = 0; v < V; v++) {
-                if (!in[v]) continue;
-                const int c = (v * T + tid) * 8;
-                float w[8], b[8], g[8], out[8];
-                if (a.post_w) get8<DT>(a.post_w, c, w);
-                if (a.post_b) get8<DT>(a.post_b, c, b);
-                if (a.gate) get8<DT>(a.gate, gr * D + c, g);
+                    for (int e = 0; e < 8; e++) p[e] *= (double)value<DT>(w, e);
+                }
+                if (a.post_b) {
+                    const Raw<DT> b = get8<DT>(a.post_b, at[v]);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) p[e] += (double)value<DT>(b, e);
+                }
+                if (a.gate) {
+                    const Raw<DT> g = get8<DT>(a.gate, gr * D + at[v]);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) p[e] *= (double)value<DT>(g, e);
+                }
+                float out[8];
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    double p = (y[v][e] - m0) * i0;
-                    if (a.post_w) p *= (double)w[e];
-                    if (a.post_b) p += (double)b[e];
-                    if (a.gate) p *= (double)g[e];
-                    r[v][e] = fma((double)a.scale, p, r[v][e]);
+                    r[v][e] = fma(scale, p[e], r[v][e]);
                     out[e] = (float)r[v][e];
                 }
-                put8<RT>(a.r_out, o + c, out);
+                if (in[v]) put8<RT>(a.r_out, o + at[v], out);
             }
         }
-        stats(r, a.pre, m1, i1);
+        stats([&](int v, int e) __attribute__((always_inline)) { return r[v][e]; }, a.pre, m1, i1);
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int c = (v * T + tid) * 8;
-            float w[8], b[8], n[8];
-            uint32_t top = 0u;
-            if (a.pre_w && in[v]) get8<DT>(a.pre_w, c, w);
-            if (a.pre_b && in[v]) get8<DT>(a.pre_b, c, b);
+            double t[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) t[e] = (r[v][e] - m1) * i1;
+            if (a.pre_w) {
+                const Raw<DT> w = get8<DT>(a.pre_w, at[v]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) t[e] *= (double)value<DT>(w, e);
+            }
+            if (a.pre_b) {
+                const Raw<DT> b = get8<DT>(a.pre_b, at[v]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) t[e] += (double)value<DT>(b, e);
+            }
+            // Two roundings differ from one only where the first gives a border between
+            // two codes or a power of two: a number whose last 19 bits are zeros.
+            float n[8];
+            uint32_t low = ~0u;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                double t = (r[v][e] - m1) * i1;
-                if (a.pre_w) t *= (double)w[e];
-                if (a.pre_b) t += (double)b[e];
-                n[e] = round_to_odd(t);
+                n[e] = (float)t[e];
+                const uint32_t b = __float_as_uint(n[e]) << 13;
+                low = b < low ? b : low;
+            }
+            if (low == 0u) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) n[e] = round_to_odd(t[e]);
+            }
+            uint32_t top = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
                 const uint32_t bits = abs_bits(n[e]);
                 top = bits > top ? bits : top;
             }
             const uint32_t s = mx_scale_byte<TYPE>(quad_max(top));      // D % 32 == 0: a quad lies in the row or past it
-            if (!in[v]) continue;
             const u32x2_t q = mx_codes8<TYPE>(n, s);
-            const int64_t piece = (o + c) >> 3;
-            if constexpr (TYPE == XT_MXFP4) reinterpret_cast<uint32_t*>(args.codes)[piece] = q[0];
-            else reinterpret_cast<u32x2_t*>(args.codes)[piece] = q;
-            if ((tid & 3) == 0) args.scales[piece >> 2] = (uint8_t)s;
+            const int64_t piece = (o + at[v]) >> 3;
+            if (in[v]) {
+                if constexpr (TYPE == XT_MXFP4) reinterpret_cast<uint32_t*>(args.codes)[piece] = q[0];
+                else reinterpret_cast<u32x2_t*>(args.codes)[piece] = q;
+                if ((tid & 3) == 0) args.scales[piece >> 2] = (uint8_t)s;
+            }
         }
         if (a.stats && tid < 4) a.stats[m * 4 + tid] = (float)(tid == 0 ? m0 : tid == 1 ? i0 : tid == 2 ? m1 : i1);
     }

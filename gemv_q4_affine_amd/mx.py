@@ -10,11 +10,12 @@ An MX tensor [R, K] is the tuple of its planes (codes, scales): uint8 codes
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from .binding import Q4_BF16, _DT, _check, _dt, lib as _base_lib
-from .block import (Q4_ACT_NONE, Q4_ACT_SILU, Q4_NORM_NONE, Q4_NORM_RMS, _code, _gate_rows, _handle, _like, _new, _out, _ptr,
+from .block import (Q4_ACT_NONE, Q4_ACT_SILU, Q4_NORM_NONE, Q4_NORM_RMS, _code, _gate_rows, _handle, _like, _new, _out,
                     _summed, _vectors, _workspace)
 
 Q4_MXFP4, Q4_MXFP8 = 8, 9
@@ -52,20 +53,45 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+# A token's calls are host-bound (a launch is 4 us, its kernel 3 to 12), so the
+# marshalling asks a tensor for little: its device, contiguity and address once.
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _run(name, args, like, stream, *tensors):
-    """The call, on the GPU of `like`, where every other tensor has to be too."""
+def _there(fn):
+    """Runs an operator on the GPU of its tensors: `fn` raises _Elsewhere where that is not the current one."""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        try:
+            return fn(*args, **kw)
+        except _Elsewhere as e:
+            with torch.cuda.device(e.args[0]):
+                return fn(*args, **kw)
+    return call
+
+
+class _Elsewhere(Exception):
+    pass
+
+
+def _here(like):
     at = like.get_device()
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.get_device() != at:
-            raise ValueError(f"{name}: tensors on different devices")
-    if at == _device():
-        _check(name, getattr(_lib, name)(*args, _handle(stream, like)))
-    else:
-        with torch.cuda.device(at):
-            _check(name, getattr(_lib, name)(*args, _handle(stream, like)))
+    if at < 0:
+        raise ValueError("tensors must live on the GPU")
+    if at != _device():
+        raise _Elsewhere(at)
+    return at
+
+
+def _p(t, at):
+    """A tensor's address (raw pointers pass through), on GPU `at`."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != at:
+        raise ValueError("tensors must live on the GPU, all on the same one")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def _mx(t, name):
@@ -73,15 +99,13 @@ def _mx(t, name):
     if len(t) != 2:
         raise ValueError(f"{name} must be (codes, scales)")
     q, s = t
-    R, groups = s.shape
-    if q.element_size() != 1 or s.element_size() != 1 or q.dim() != 2 or q.shape[0] != R:
-        raise ValueError(f"the planes of {name} do not fit each other")
-    width = q.shape[1]
-    if width == groups * 16:
-        return Q4_MXFP4, R, groups * 32
-    if width != groups * 32:
-        raise ValueError(f"the planes of {name} do not fit each other")
-    return Q4_MXFP8, R, width
+    (rows, width), (R, groups) = q.shape, s.shape
+    if rows == R and q.element_size() == 1 and s.element_size() == 1:
+        if width == groups * 16:
+            return Q4_MXFP4, R, groups * 32
+        if width == groups * 32:
+            return Q4_MXFP8, R, width
+    raise ValueError(f"the planes of {name} do not fit each other")
 
 
 def _weight(w, name="w"):
@@ -101,8 +125,9 @@ def _pair(gate, up):
 def _x(x, K, dtype):
     """(type, rows, planes, the tensor itself or its codes, output dtype) of an activation."""
     if isinstance(x, torch.Tensor):
-        M = x.shape[0]
-        _like(x, "x", (M, K), x.dtype)
+        M, width = x.shape
+        if width != K:
+            raise ValueError(f"x must have {K} values a row, not {width}")
         if dtype is not None and dtype != x.dtype:
             raise ValueError(f"dtype must be x's, {x.dtype}")
         return _dt(x), M, (x, None), x, x.dtype
@@ -116,25 +141,27 @@ def _x(x, K, dtype):
 
 # ---- planes ---------------------------------------------------------------------
 
+@_there
 def mx_quantize(v, type=Q4_MXFP8, codes=None, scales=None, stream=None):
     """The planes (codes, scales) of v [M, K] as Q4_MXFP8 or Q4_MXFP4."""
-    lib()
     M, K = v.shape
     if K % 32:
         raise ValueError(f"{K} values a row: not whole blocks of 32")
+    at = _here(v)
     codes = _out(codes, "codes", (M, K // 2 if type == Q4_MXFP4 else K), torch.uint8, v, stream)
     scales = _out(scales, "scales", (M, K // 32), torch.uint8, v, stream)
-    _run("mx_quantize", (_ptr(v), _dt(v), type, _ptr(codes), _ptr(scales), M, K), v, stream, codes, scales)
+    _check("mx_quantize", lib().mx_quantize(_p(v, at), _dt(v), type, _p(codes, at), _p(scales, at), M, K, _handle(stream, v)))
     return codes, scales
 
 
+@_there
 def mx_dequantize(planes, dtype=torch.bfloat16, v=None, stream=None):
     """The values [M, K] that planes stand for."""
-    lib()
     kind, M, K = _mx(planes, "planes")
+    at = _here(planes[0])
     v = _out(v, "v", (M, K), dtype, planes[0], stream)
-    _run("mx_dequantize", (kind, _ptr(planes[0]), _ptr(planes[1]), _ptr(v), _code(dtype), M, K), planes[0], stream,
-         planes[1], v)
+    _check("mx_dequantize", lib().mx_dequantize(kind, _p(planes[0], at), _p(planes[1], at), _p(v, at), _code(dtype), M, K,
+                                                _handle(stream, planes[0])))
     return v
 
 
@@ -144,6 +171,7 @@ def mx_linear_workspace_size(M, N, K, x_type=Q4_MXFP8) -> int:
     return int(lib().mx_linear_workspace_size(x_type, M, N, K))
 
 
+@_there
 def mx_linear(w, x, bias=None, act=Q4_ACT_NONE, residual=None, save_pre=False, dtype=None, y=None, pre=None,
               workspace="auto", stream=None):
     """y [M, N] = act(x . W^T + bias) + residual of `dtype` (x's; for MX x
@@ -151,6 +179,7 @@ def mx_linear(w, x, bias=None, act=Q4_ACT_NONE, residual=None, save_pre=False, d
     before the activation: (y, pre)."""
     N, K = _weight(w)
     xt, M, (xq, xs), like, dtype = _x(x, K, dtype)
+    at = _here(like)
     _like(bias, "bias", (N,), dtype)
     _like(residual, "residual", (M, N), dtype)
     y = _out(y, "y", (M, N), dtype, like, stream)
@@ -158,8 +187,9 @@ def mx_linear(w, x, bias=None, act=Q4_ACT_NONE, residual=None, save_pre=False, d
         pre = _new((M, N), dtype, like, stream)
     _like(pre, "pre", (M, N), dtype)
     ws, n = _workspace(workspace, mx_linear_workspace_size(M, N, K, xt), like, stream)
-    _run("mx_linear", (_ptr(w[0]), _ptr(w[1]), _ptr(bias), act, _ptr(residual), xt, _ptr(xq), _ptr(xs), _code(dtype), _ptr(y),
-                       _ptr(pre), M, N, K, _ptr(ws), n), like, stream, w[0], w[1], xs, bias, residual, y, pre, ws)
+    _check("mx_linear", lib().mx_linear(_p(w[0], at), _p(w[1], at), _p(bias, at), act, _p(residual, at), xt, _p(xq, at),
+                                        _p(xs, at), _code(dtype), _p(y, at), _p(pre, at), M, N, K, _p(ws, at), n,
+                                        _handle(stream, like)))
     return y if pre is None else (y, pre)
 
 
@@ -167,12 +197,13 @@ def mx_linear_backward_workspace_size(M, N, K) -> int:
     return int(lib().mx_linear_backward_workspace_size(M, N, K))
 
 
+@_there
 def mx_linear_backward(w, dy, act=Q4_ACT_NONE, pre=None, bias_grad=False, dx=None, dz=None, dbias=None,
                        workspace="auto", stream=None):
     """Gradients {"dx", "dz" (with an activation), "dbias" (with bias_grad)}
     of mx_linear; the residual's gradient is dy itself."""
     N, K = _weight(w)
-    M = dy.shape[0]
+    M, at = dy.shape[0], _here(dy)
     _like(dy, "dy", (M, N), dy.dtype)
     _like(pre, "pre", (M, N), dy.dtype)
     out = {"dx": _summed(dx, "dx", (M, K), dy.dtype, N, dy, stream)}
@@ -181,9 +212,10 @@ def mx_linear_backward(w, dy, act=Q4_ACT_NONE, pre=None, bias_grad=False, dx=Non
     if bias_grad or dbias is not None:
         out["dbias"] = _summed(dbias, "dbias", (N,), torch.float32, M, dy, stream)
     ws, n = _workspace(workspace, mx_linear_backward_workspace_size(M, N, K), dy, stream)
-    _run("mx_linear_backward", (_ptr(w[0]), _ptr(w[1]), act, _ptr(pre), _ptr(dy), _dt(dy), _ptr(out["dx"]),
-                                _ptr(out.get("dz")), _ptr(out.get("dbias")), M, N, K, _ptr(ws), n), dy, stream, w[0], w[1],
-         pre, ws, *out.values())
+    _check("mx_linear_backward",
+           lib().mx_linear_backward(_p(w[0], at), _p(w[1], at), act, _p(pre, at), _p(dy, at), _dt(dy), _p(out["dx"], at),
+                                    _p(out.get("dz"), at), _p(out.get("dbias"), at), M, N, K, _p(ws, at), n,
+                                    _handle(stream, dy)))
     return out
 
 
@@ -193,12 +225,14 @@ def mx_gated_workspace_size(M, N, K, x_type=Q4_MXFP8) -> int:
     return int(lib().mx_gated_workspace_size(x_type, M, N, K))
 
 
+@_there
 def mx_gated(gate, up, x, act=Q4_ACT_SILU, gate_bias=None, up_bias=None, save_pre=False, dtype=None, h=None,
              gate_pre=None, up_pre=None, workspace="auto", stream=None):
     """h [M, N] = act(x . Wgate^T + gate_bias) * (x . Wup^T + up_bias); with
     save_pre (or both tensors) also the two projections: (h, gate_pre, up_pre)."""
     N, K = _pair(gate, up)
     xt, M, (xq, xs), like, dtype = _x(x, K, dtype)
+    at = _here(like)
     _like(gate_bias, "gate_bias", (N,), dtype)
     _like(up_bias, "up_bias", (N,), dtype)
     h = _out(h, "h", (M, N), dtype, like, stream)
@@ -208,9 +242,9 @@ def mx_gated(gate, up, x, act=Q4_ACT_SILU, gate_bias=None, up_bias=None, save_pr
     _like(gate_pre, "gate_pre", (M, N), dtype)
     _like(up_pre, "up_pre", (M, N), dtype)
     ws, n = _workspace(workspace, mx_gated_workspace_size(M, N, K, xt), like, stream)
-    _run("mx_gated", (_ptr(gate[0]), _ptr(gate[1]), _ptr(up[0]), _ptr(up[1]), _ptr(gate_bias), _ptr(up_bias), act, xt, _ptr(xq),
-                      _ptr(xs), _code(dtype), _ptr(h), _ptr(gate_pre), _ptr(up_pre), M, N, K, _ptr(ws), n), like, stream,
-         gate[0], gate[1], up[0], up[1], gate_bias, up_bias, xs, h, gate_pre, up_pre, ws)
+    _check("mx_gated", lib().mx_gated(_p(gate[0], at), _p(gate[1], at), _p(up[0], at), _p(up[1], at), _p(gate_bias, at),
+                                      _p(up_bias, at), act, xt, _p(xq, at), _p(xs, at), _code(dtype), _p(h, at),
+                                      _p(gate_pre, at), _p(up_pre, at), M, N, K, _p(ws, at), n, _handle(stream, like)))
     return h if gate_pre is None else (h, gate_pre, up_pre)
 
 
@@ -218,11 +252,12 @@ def mx_gated_backward_workspace_size(M, N, K) -> int:
     return int(lib().mx_gated_backward_workspace_size(M, N, K))
 
 
+@_there
 def mx_gated_backward(gate, up, dh, gate_pre, up_pre, act=Q4_ACT_SILU, bias_grad=False, dx=None, dgate=None, dup=None,
                       dgate_bias=None, dup_bias=None, workspace="auto", stream=None):
     """Gradients {"dx", "dgate", "dup", and with bias_grad "dgate_bias", "dup_bias"} of mx_gated."""
     N, K = _pair(gate, up)
-    M = dh.shape[0]
+    M, at = dh.shape[0], _here(dh)
     for t, name in ((dh, "dh"), (gate_pre, "gate_pre"), (up_pre, "up_pre"), (dgate, "dgate"), (dup, "dup")):
         _like(t, name, (M, N), dh.dtype)
     out = {"dx": _summed(dx, "dx", (M, K), dh.dtype, N, dh, stream),
@@ -232,15 +267,17 @@ def mx_gated_backward(gate, up, dh, gate_pre, up_pre, act=Q4_ACT_SILU, bias_grad
         if bias_grad or t is not None:
             out[name] = _summed(t, name, (N,), torch.float32, M, dh, stream)
     ws, n = _workspace(workspace, mx_gated_backward_workspace_size(M, N, K), dh, stream)
-    _run("mx_gated_backward", (_ptr(gate[0]), _ptr(gate[1]), _ptr(up[0]), _ptr(up[1]), act, _ptr(gate_pre), _ptr(up_pre),
-                               _ptr(dh), _dt(dh), _ptr(out["dx"]), _ptr(out["dgate"]), _ptr(out["dup"]),
-                               _ptr(out.get("dgate_bias")), _ptr(out.get("dup_bias")), M, N, K, _ptr(ws), n), dh, stream,
-         gate[0], gate[1], up[0], up[1], gate_pre, up_pre, ws, *out.values())
+    _check("mx_gated_backward",
+           lib().mx_gated_backward(_p(gate[0], at), _p(gate[1], at), _p(up[0], at), _p(up[1], at), act, _p(gate_pre, at),
+                                   _p(up_pre, at), _p(dh, at), _dt(dh), _p(out["dx"], at), _p(out["dgate"], at),
+                                   _p(out["dup"], at), _p(out.get("dgate_bias"), at), _p(out.get("dup_bias"), at), M, N, K,
+                                   _p(ws, at), n, _handle(stream, dh)))
     return out
 
 
 # ---- norm -----------------------------------------------------------------------
 
+@_there
 def block_norm_mx(r, y=None, pre_norm=Q4_NORM_RMS, pre_weight=None, pre_bias=None, post_norm=Q4_NORM_NONE,
                   post_weight=None, post_bias=None, gate=None, gate_rows=None, scale=1.0, eps=1e-5, n_type=Q4_MXFP8,
                   save_stats=False, dtype=None, r_out=None, n=None, stats=None, stream=None):
@@ -248,10 +285,10 @@ def block_norm_mx(r, y=None, pre_norm=Q4_NORM_RMS, pre_weight=None, pre_bias=Non
 
     stats (float32 [M, 4], for block_norm_backward) is None unless asked for;
     without y, r' is r itself and `dtype` the type of the weights (r's)."""
-    lib()
     M, D = r.shape
     if D % 32:
         raise ValueError(f"{D} values a row: not whole blocks of 32")
+    at = _here(r)
     dt = y.dtype if y is not None else (dtype or r.dtype)
     if y is not None:
         _like(y, "y", (M, D), dt)
@@ -266,8 +303,8 @@ def block_norm_mx(r, y=None, pre_norm=Q4_NORM_RMS, pre_weight=None, pre_bias=Non
     if stats is None and save_stats:
         stats = _new((M, 4), torch.float32, r, stream)
     _like(stats, "stats", (M, 4), torch.float32)
-    _run("block_norm_mx", (_ptr(y), _ptr(r), _code(dt), _dt(r), M, D, post_norm, _ptr(post_weight), _ptr(post_bias), _ptr(gate),
-                           rows, scale, pre_norm, _ptr(pre_weight), _ptr(pre_bias), eps, _ptr(r_out), n_type, _ptr(codes),
-                           _ptr(scales), _ptr(stats)), r, stream, y, post_weight, post_bias, gate, pre_weight, pre_bias,
-         r_out, codes, scales, stats)
+    _check("block_norm_mx",
+           lib().block_norm_mx(_p(y, at), _p(r, at), _code(dt), _dt(r), M, D, post_norm, _p(post_weight, at), _p(post_bias, at),
+                               _p(gate, at), rows, scale, pre_norm, _p(pre_weight, at), _p(pre_bias, at), eps, _p(r_out, at),
+                               n_type, _p(codes, at), _p(scales, at), _p(stats, at), _handle(stream, r)))
     return r if y is None else r_out, (codes, scales), stats
