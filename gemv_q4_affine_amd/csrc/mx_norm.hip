@@ -129,17 +129,29 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
                     for (int e = 0; e < 8; e++) s += x(v, e);
             mean = row_sum(s) * inv;
             s = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                if (in[v])
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const double d = x(v, e) - mean;
+                        s = fma(d, d, s);
+                    }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                if (in[v])
+#pragma unroll
+                    for (int e = 0; e < 8; e++) s = fma(x(v, e), x(v, e), s);
         }
-#pragma unroll
-        for (int v = 0; v < V; v++)
-            if (in[v])
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const double d = x(v, e) - mean;
-                    s = fma(d, d, s);
-                }
         rstd = 1.0 / sqrt(fma(row_sum(s), inv, (double)a.eps));
     };
+    // one piece a thread: the weights stay in registers; more of them are read again
+    Raw<DT> pre_w = {}, post_w = {};
+    if constexpr (V == 1) {
+        if (a.pre_w) pre_w = get8<DT>(a.pre_w, at[0]);
+        if (a.post_w) post_w = get8<DT>(a.post_w, at[0]);
+    }
     Raw<RT> nr[V];
     Raw<DT> ny[V];
     auto request = [&](int64_t m) __attribute__((always_inline)) {
@@ -163,6 +175,8 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
         if (m + gridDim.x < a.M) request(m + gridDim.x);
         if (a.y) {
             const int64_t gr = a.gate_rows >= a.M ? 0 : (uint32_t)m / (uint32_t)a.gate_rows;
+            Raw<DT> gate = {};
+            if (V == 1 && a.gate) gate = get8<DT>(a.gate, gr * D + at[0]);
             stats([&](int v, int e) __attribute__((always_inline)) { return (double)value<DT>(y[v], e); }, a.post, m0, i0);
             const double scale = (double)a.scale;
 #pragma unroll
@@ -170,9 +184,17 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
                 // scale gate ((y - mean) rstd w + b)
                 double p[8];
 #pragma unroll
-                for (int e = 0; e < 8; e++) p[e] = ((double)value<DT>(y[v], e) - m0) * i0;
+                for (int e = 0; e < 8; e++) p[e] = (double)value<DT>(y[v], e);
+                if (a.post == NORM_LAYER) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) p[e] -= m0;
+                }
+                if (a.post != NORM_NONE) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) p[e] *= i0;
+                }
                 if (a.post_w) {
-                    const Raw<DT> w = get8<DT>(a.post_w, at[v]);
+                    const Raw<DT> w = V == 1 ? post_w : get8<DT>(a.post_w, at[v]);
 #pragma unroll
                     for (int e = 0; e < 8; e++) p[e] *= (double)value<DT>(w, e);
                 }
@@ -182,7 +204,7 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
                     for (int e = 0; e < 8; e++) p[e] += (double)value<DT>(b, e);
                 }
                 if (a.gate) {
-                    const Raw<DT> g = get8<DT>(a.gate, gr * D + at[v]);
+                    const Raw<DT> g = V == 1 ? gate : get8<DT>(a.gate, gr * D + at[v]);
 #pragma unroll
                     for (int e = 0; e < 8; e++) p[e] *= (double)value<DT>(g, e);
                 }
@@ -200,9 +222,15 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
         for (int v = 0; v < V; v++) {
             double t[8];
 #pragma unroll
-            for (int e = 0; e < 8; e++) t[e] = (r[v][e] - m1) * i1;
+            for (int e = 0; e < 8; e++) t[e] = r[v][e];
+            if (a.pre == NORM_LAYER) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) t[e] -= m1;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) t[e] *= i1;
             if (a.pre_w) {
-                const Raw<DT> w = get8<DT>(a.pre_w, at[v]);
+                const Raw<DT> w = V == 1 ? pre_w : get8<DT>(a.pre_w, at[v]);
 #pragma unroll
                 for (int e = 0; e < 8; e++) t[e] *= (double)value<DT>(w, e);
             }
@@ -248,7 +276,7 @@ template <int DT, int RT, int V>
 static void norm_v(const MxNormArgs& a, hipStream_t s) {
     const int64_t D = a.norm.D, M = a.norm.M;
     const unsigned threads = (unsigned)((D / 8 + 64 * V - 1) / (64 * V) * 64);
-    const int64_t fit = (int64_t)current_cu_count() * ((V == 1 ? 2048 : 1024) / threads);
+    const int64_t fit = (int64_t)current_cu_count() * (1280 / threads > 0 ? 1280 / threads : 1);
     auto k = a.n_type == XT_MXFP4 ? k_block_norm_mx<DT, RT, V, XT_MXFP4> : k_block_norm_mx<DT, RT, V, XT_MXFP8>;
     hipLaunchKernelGGL(k, dim3((unsigned)(M < fit ? M : fit)), dim3(threads), 0, s, a);
 }
