@@ -13,8 +13,9 @@
 // rows by 64 bytes (8 rows by 128 at 8 bits), so that four (eight) neighbouring
 // lanes read whole lines, and the 16-byte pieces of a row are placed by an XOR with
 // the row, so that the reads of an operand, 32 rows apart by a row's pitch, meet no
-// bank twice.  The scales come from images (k_mx_scales), a dword for lane and 256
-// k, and pass through LDS too.  What a copy would read past a row's end or behind
+// bank twice.  The scales pass through LDS too, eight bytes a row and 256 k, which a
+// shift by 8 h bits brings to the bytes that the instructions take (0 and 2 of
+// either dword: blocks h, 2 + h, 4 + h, 6 + h).  What a copy would read past a row's end or behind
 // the last row it takes from the row's last piece or from the last row: those
 // blocks have the scale 2^-127 on both sides (nothing is left of their
 // products), those rows are never stored.
@@ -28,51 +29,49 @@ namespace {
 constexpr int kRing = 3;
 constexpr int kScaleUnit = 256;            // bytes of a panel's scales for 256 k
 
+// copy_unit for four bytes a lane.
+__device__ __forceinline__ void copy_dwords(const uint8_t* src, uint32_t voff, uint32_t m0) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(src), "s"(m0) : "memory", "m0");
+}
+
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// An address that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
+}
 
 }  // namespace
 
 // ---- scales ----------------------------------------------------------------------
 //
-// [t = k / 256][panel][lane]: byte s of the dword is the scale of row lane & 31 of
-// the panel, block 8 t + 2 s + (lane >> 5): what the instruction s of those 256 k
-// takes.  Blocks past K and rows past the last are 0.  A thread takes 512 k of a
-// row, 16 neighbouring scales.
+// A group of 256 k takes eight neighbouring scales of a row.  Where K is a multiple
+// of 256 they are copied from the planes, else from images of them, [k / 256][row][8]
+// with zeros past K: a thread takes a row's eight.
 __global__ __launch_bounds__(256) void k_mx_scales(const MxTileArgs a) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t pairs = (a.groups + 1) / 2, row_id = id >> 5;
-    const int64_t panel = row_id / pairs, t = row_id % pairs * 2;
-    if (panel >= a.w_pad + a.x_pad) return;
-    const bool is_w = panel < a.w_pad;
-    const int64_t p = is_w ? panel : panel - a.w_pad, rows = is_w ? a.N : a.epi.M;
-    const uint8_t* s = is_w ? a.ws[a.nmat == 2 ? p & 1 : 0] : a.xs;
-    const int64_t row = (is_w ? p / a.nmat : p) * 32 + (id & 31), nb = a.K / 32, first = t * 8;
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if (row < rows) {
-        const uint8_t* q = s + row * nb + first;
-        typedef u32x4_t u32x4_b __attribute__((aligned(1)));
-        if (first + 16 <= nb) {
-            const u32x4_t r = *reinterpret_cast<const u32x4_b*>(q);
+    const int64_t all = a.N * a.nmat + a.epi.M, t = id / all, i = id % all, nb = a.K / 32;
+    if (t >= a.groups) return;
+    const bool is_w = i < a.N * a.nmat;
+    const int mat = is_w && i >= a.N ? 1 : 0;
+    const int64_t row = is_w ? i - mat * a.N : i - a.N * a.nmat;
+    const uint8_t* s = (is_w ? a.ws[mat] : a.xs) + row * nb;
+    u32x2_t v = {0u, 0u};
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = r[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; e++)
-                if (first + e < nb) v[e >> 2] |= (uint32_t)q[e] << (8 * (e & 3));
-        }
-    }
-    uint32_t* img = is_w ? a.w_scales : a.x_scales;
-    const int64_t panels = is_w ? a.w_pad : a.x_pad;
-#pragma unroll
-    for (int g = 0; g < 2; g++) {
-        if (t + g >= a.groups) break;
-        uint32_t* out = img + ((t + g) * panels + p) * 64 + (id & 31);
-        out[0] = __builtin_amdgcn_perm(v[2 * g + 1], v[2 * g], 0x06040200u);
-        out[32] = __builtin_amdgcn_perm(v[2 * g + 1], v[2 * g], 0x07050301u);
-    }
+    for (int e = 0; e < 8; e++)
+        if (8 * t + e < nb) v[e >> 2] |= (uint32_t)s[8 * t + e] << (8 * (e & 3));
+    reinterpret_cast<u32x2_t*>(a.scales)[t * all + i] = v;
 }
 
 // ---- the product -------------------------------------------------------------------
+
+template <int NT, int MT, int EPI>
+constexpr int wave_lds() {
+    if constexpr (EPI == EPI_GATED) return 0;
+    else return RowEpilogue<NT, MT, EPI>::kWaveB;
+}
 
 template <int NT, int MT, int XT, int EPI>
 __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
@@ -83,9 +82,10 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
     constexpr int kSlot = 2 * NT * kWPanel + 2 * MT * kXPanel;
     constexpr int kCopies = NT + MT * kXR;                  // of a wave and step, without the scales'
     constexpr int kScaleSlot = 2 * (NT + MT) * kScaleUnit;  // of two steps
-    constexpr int kRowF = tile_row_floats<NT>();
-    constexpr int kData = kRing * kSlot, kLoop = kData + 2 * kScaleSlot, kTail = 4 * 32 * kRowF * 4;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLoop > kTail ? kLoop : kTail];
+    constexpr int kData = kRing * kSlot, kLoop = kData + 2 * kScaleSlot;
+    constexpr int kWaveB = wave_lds<NT, MT, EPI>();          // the epilogue's tiles lie where the operands were
+    constexpr int kScaleCopies = (NT + MT) / 2;             // of a wave and two steps
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLoop > 4 * kWaveB ? kLoop : 4 * kWaveB];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -94,46 +94,49 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
 
     // ---- the tile: workgroup b runs on XCD b mod 8; consecutive tiles v go to one
     // XCD, down the rows first, in groups of eight row tiles (as in tile_gemm.hip) ----
-    const int64_t x_panels = (a.epi.M + 31) / 32;
-    const int64_t tiles_n = (a.w_panels + 2 * NT - 1) / (2 * NT), tiles_m = (x_panels + 2 * MT - 1) / (2 * MT);
-    const int64_t G = gridDim.x, xcd = blockIdx.x % 8, each = G / 8, rest = G % 8;
-    int64_t v = xcd * each + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
-    const int part = (int)(v / (tiles_n * tiles_m));
-    v -= part * (tiles_n * tiles_m);
-    const int64_t group = v / (8 * tiles_n), left_m = tiles_m - group * 8;
-    const int64_t high = left_m < 8 ? left_m : 8;
+    // (counts of panels and tiles stay below 2^31: the launch's own limits)
+    const uint32_t w_panels = (uint32_t)a.w_panels, x_panels = (uint32_t)((a.epi.M + 31) / 32);
+    const uint32_t tiles_n = (w_panels + 2 * NT - 1) / (2 * NT), tiles_m = (x_panels + 2 * MT - 1) / (2 * MT);
+    const uint32_t G = gridDim.x, xcd = blockIdx.x % 8, each = G / 8, rest = G % 8;
+    uint32_t v = xcd * each + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+    const int part = a.parts > 1 ? (int)(v / (tiles_n * tiles_m)) : 0;
+    v -= (uint32_t)part * (tiles_n * tiles_m);
+    const uint32_t group = v / (8 * tiles_n), left_m = tiles_m - group * 8;
+    const uint32_t high = left_m < 8 ? left_m : 8;
     v -= group * 8 * tiles_n;
-    const int64_t pn0 = v / high * (2 * NT), pm0 = (group * 8 + v % high) * (2 * MT);
+    const uint32_t pn0 = v / high * (2 * NT), pm0 = (group * 8 + v % high) * (2 * MT);
 
     // ---- copies.  The sum's groups of 256 k (two steps) t0 .. of this part ----
-    const int64_t t0 = a.groups * part / a.parts, t1 = a.groups * (part + 1) / a.parts;
-    const int64_t all_steps = (a.K + 127) / 128;
-    const int S = (int)((2 * t1 < all_steps ? 2 * t1 : all_steps) - 2 * t0);
+    const uint32_t groups = (uint32_t)a.groups;
+    const int t0 = (int)((uint64_t)groups * part / a.parts), t1 = (int)((uint64_t)groups * (part + 1) / a.parts);
+    const int S = 2 * (t1 - t0);                             // steps; one wholly past K has scales of zero
     const uint32_t row_w = (uint32_t)(a.K / 2), row_x = (uint32_t)(k8 ? a.K : a.K / 2);
+    const uint32_t rows_w = (uint32_t)a.N, rows_x = (uint32_t)a.epi.M;
     const uint8_t* src[kCopies];                            // the first row of a copy's unit
     uint32_t at[kCopies];                                   // the lane's row in it, in bytes
 #pragma unroll
     for (int t = 0; t < kCopies; t++) {
         const bool w = t < NT;
         // unit 4 t + wave of the tile's W (x): 16 rows of a panel, 8 at 8 bits
-        const int u = (w ? t : t - NT) * 4 + wave, per = w || !k8 ? 2 : 4, height = 32 / per;
-        int64_t p = (w ? pn0 : pm0) + u / per;
-        const int64_t last_p = (w ? a.w_panels : x_panels) - 1;
+        const uint32_t u = (uint32_t)((w ? t : t - NT) * 4 + wave), per = w || !k8 ? 2 : 4, height = 32 / per;
+        uint32_t p = (w ? pn0 : pm0) + u / per;
+        const uint32_t last_p = (w ? w_panels : x_panels) - 1;
         p = p < last_p ? p : last_p;
-        const uint8_t* base = w ? a.wq[a.nmat == 2 ? p & 1 : 0] : a.xq;
-        const int64_t rows = w ? a.N : a.epi.M, pitch = w ? row_w : row_x;
-        int64_t first = (w ? p / a.nmat : p) * 32 + u % per * height;
+        const bool up = w && a.nmat == 2 && (p & 1);
+        const uint8_t* base = w ? (up ? a.wq[1] : a.wq[0]) : a.xq;
+        const uint32_t rows = w ? rows_w : rows_x, pitch = w ? row_w : row_x;
+        uint32_t first = (w && a.nmat == 2 ? p >> 1 : p) * 32 + u % per * height;
         first = first < rows ? first : rows - 1;
-        const int64_t in = rows - 1 - first, r = lane / (64 / height);
-        src[t] = base + first * pitch;
-        at[t] = (uint32_t)((r < in ? r : in) * pitch);
+        const uint32_t in = rows - 1 - first, r = (uint32_t)lane / (64 / height);
+        src[t] = base + (uint64_t)first * pitch;
+        at[t] = (r < in ? r : in) * pitch;
     }
     // the lane's piece of a row: the XOR is by the row mod 16 (the unit's parity at 8 bits)
     const int wr = lane >> 2, xr = k8 ? (lane >> 3) + 8 * (wave & 1) : wr;
     auto swz4 = [](int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); };
     auto swz8 = [](int r) { return (r & 7) ^ ((r >> 3) & 1); };
-    const uint32_t piece_w = (uint32_t)((lane & 3) ^ swz4(wr)) + (uint32_t)(8 * t0);
-    const uint32_t piece_x = k8 ? (uint32_t)((lane & 7) ^ swz8(xr)) + (uint32_t)(16 * t0) : piece_w;
+    const uint32_t piece_w = (uint32_t)(((lane & 3) ^ swz4(wr)) + 8 * t0);
+    const uint32_t piece_x = k8 ? (uint32_t)(((lane & 7) ^ swz8(xr)) + 16 * t0) : piece_w;
     const uint32_t last_w = row_w / 16 - 1, last_x = row_x / 16 - 1;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds);
     // The step that copies stand at; after the last one it is copied again (and
@@ -151,16 +154,27 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         copy_unit(src[t], at[t] + (w ? off_w : off_x),
                   lds0 + (uint32_t)(slot * kSlot + (w ? 0 : 2 * NT * kWPanel) + ((w ? t : t - NT) * 4 + wave) * 1024));
     };
-    // the scales of a group of 256 k: NT / 2 units of 1 KiB of W, MT / 2 of x; a wave
-    // copies one (some twice)
-    constexpr int kUnitsW = NT / 2, kUnitsS = NT / 2 + MT / 2;
-    const int su = wave < kUnitsS ? wave : 0;
-    const uint32_t* s_src = su < kUnitsW ? a.w_scales + (pn0 * 64 + su * 256) : a.x_scales + (pm0 * 64 + (su - kUnitsW) * 256);
-    const int64_t s_pitch = (su < kUnitsW ? a.w_pad : a.x_pad) * 64;
+    // the scales of a group: a copy is a panel's 32 rows by eight bytes
+    const uint8_t* s_src[kScaleCopies];
+    uint32_t s_at[kScaleCopies];
+#pragma unroll
+    for (int t = 0; t < kScaleCopies; t++) {
+        const uint32_t u = (uint32_t)(t * 4 + wave);          // panel of the tile: W, then x
+        const bool w = u < 2 * NT;
+        uint32_t p = w ? pn0 + u : pm0 + u - 2 * NT;
+        const uint32_t last_p = (w ? w_panels : x_panels) - 1;
+        p = p < last_p ? p : last_p;
+        const bool up = w && a.nmat == 2 && (p & 1);
+        const uint32_t first = (w && a.nmat == 2 ? p >> 1 : p) * 32, in = (w ? rows_w : rows_x) - 1 - first, r = (uint32_t)lane >> 1;
+        s_src[t] = scalar((w ? (up ? a.w_scales[1] : a.w_scales[0]) : a.x_scales) + (uint64_t)first * a.scale_row);
+        s_at[t] = (r < in ? r : in) * a.scale_row + (uint32_t)(lane & 1) * 4;
+    }
     auto copy_scales = [&](int g) __attribute__((always_inline)) {       // group g of this part
-        const int64_t t = t0 + g < t1 ? t0 + g : t1 - 1;
-        copy_unit(reinterpret_cast<const uint8_t*>(s_src + t * s_pitch), (uint32_t)lane * 16,
-                  lds0 + (uint32_t)(kData + (g & 1) * kScaleSlot + su * 1024));
+        const int t = t0 + g < t1 ? t0 + g : t1 - 1;
+#pragma unroll
+        for (int e = 0; e < kScaleCopies; e++)
+            copy_dwords(scalar(s_src[e] + (int64_t)t * a.scale_group), s_at[e],
+                        lds0 + (uint32_t)(kData + (g & 1) * kScaleSlot + (e * 4 + wave) * kScaleUnit));
     };
 
     floatx16_t acc[NT][MT];
@@ -197,13 +211,14 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
             fr.x[j][e] = *reinterpret_cast<const u32x4_t*>(slot + at_x[kk][e] + j * kXPanel);
         }
     };
-    uint32_t sc[NT + MT], next_sc[NT + MT];
-    auto read_scales = [&](int g, uint32_t (&to)[NT + MT]) __attribute__((always_inline)) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(lds + kData + (g & 1) * kScaleSlot);
+    typedef uint64_t scale_t;
+    scale_t sc[NT + MT], next_sc[NT + MT];
+    auto read_scales = [&](int g, scale_t (&to)[NT + MT]) __attribute__((always_inline)) {
+        const scale_t* p = reinterpret_cast<const scale_t*>(lds + kData + (g & 1) * kScaleSlot);
 #pragma unroll
-        for (int i = 0; i < NT; i++) to[i] = p[(wn * NT + i) * 64 + lane];
+        for (int i = 0; i < NT; i++) to[i] = p[(wn * NT + i) * 32 + r];
 #pragma unroll
-        for (int j = 0; j < MT; j++) to[NT + j] = p[(2 * NT + wm * MT + j) * 64 + lane];
+        for (int j = 0; j < MT; j++) to[NT + j] = p[(2 * NT + wm * MT + j) * 32 + r];
     };
     auto mfma = [&](int q, const Frags& fr, auto byte) __attribute__((always_inline)) {
         constexpr int kByte = decltype(byte)::value;
@@ -215,8 +230,9 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
             x[e] = (int)fr.x[j][0][e];
             if constexpr (k8) x[4 + e] = (int)fr.x[j][1][e];
         }
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc[i][j], 4, k8 ? 0 : 4, kByte, (int)sc[i], kByte,
-                                                                    (int)sc[NT + j]);
+        constexpr int kOp = 2 * (kByte & 1), kDword = 32 * (kByte >> 1);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc[i][j], 4, k8 ? 0 : 4, kOp, (int)(sc[i] >> kDword),
+                                                                    kOp, (int)(sc[NT + j] >> kDword));
     };
 
     // ---- the schedule of a step: T MFMAs, the reads and copies between them ----
@@ -239,7 +255,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         for (int q = 0; q < T; q++) {
             if (q == B) {
                 // the next step has landed (and its scales), the one after it is in flight
-                step_barrier<kCopies + (kOdd ? 0 : 1)>();
+                step_barrier<kCopies + (kOdd ? 0 : kScaleCopies)>();
                 ahead++;
                 stand();
                 __builtin_amdgcn_sched_barrier(0);
@@ -267,7 +283,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         }
         if constexpr (kOdd) {
 #pragma unroll
-            for (int e = 0; e < NT + MT; e++) sc[e] = next_sc[e];
+            for (int e = 0; e < NT + MT; e++) sc[e] = next_sc[e] >> (8 * h);
         }
     };
 
@@ -285,20 +301,34 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         step_barrier<kCopies + kAfter>();
         read_scales(0, sc);
 #pragma unroll
+        for (int e = 0; e < NT + MT; e++) sc[e] >>= 8 * h;
+#pragma unroll
         for (int f = 0; f < kEarly; f++) read(f, lds, 0, fa);
-        int i = 0;
-        for (; i + 1 < S; i += 2) {
+        for (int i = 0; i < S; i += 2) {
             step(i, std::integral_constant<int, 0>{});
             step(i + 1, std::integral_constant<int, 1>{});
         }
-        if (i < S) step(i, std::integral_constant<int, 0>{});
     }
 
     // every copy has landed and every wave has read its last fragments
     step_barrier<0>();
-    tile_epilogue<NT, MT, EPI>(acc, reinterpret_cast<float*>(lds) + wave * 32 * kRowF, a.epi, a.part, part, a.w_panels,
-                               EPI == EPI_GATED ? (pn0 + wn * NT) * 16 : (pn0 + wn * NT) * 32, (pm0 + wm * MT) * 32,
-                               [](int64_t) __attribute__((always_inline)) { return 1.0f; });
+    const int64_t n0 = (int64_t)(pn0 + wn * NT) * (EPI == EPI_GATED ? 16 : 32), m0 = (int64_t)(pm0 + wm * MT) * 32;
+    auto finish = [&](auto vec, auto dtype) __attribute__((always_inline)) {
+        constexpr bool kVec = decltype(vec)::value;
+        constexpr int kDt = decltype(dtype)::value;
+        if constexpr (EPI == EPI_GATED) gate_epilogue<NT, MT, kVec, kDt>(acc, a.epi, n0, m0);
+        else row_epilogue<NT, MT, EPI, kVec, kDt>(acc, lds + wave * kWaveB, a.epi, a.part, part, a.w_panels, n0, m0);
+    };
+    using std::integral_constant;
+    if constexpr (EPI == EPI_PARTIAL) {
+        finish(integral_constant<bool, true>{}, integral_constant<int, DT_F32>{});
+    } else if (a.epi.dtype == DT_BF16) {
+        if (a.epi.N % 8 == 0) finish(integral_constant<bool, true>{}, integral_constant<int, DT_BF16>{});
+        else finish(integral_constant<bool, false>{}, integral_constant<int, DT_BF16>{});
+    } else {
+        if (a.epi.N % 8 == 0) finish(integral_constant<bool, true>{}, integral_constant<int, DT_F16>{});
+        else finish(integral_constant<bool, false>{}, integral_constant<int, DT_F16>{});
+    }
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -306,7 +336,6 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
 namespace {
 
 int64_t panels_of(int64_t rows) { return (rows + 31) / 32; }
-int64_t padded(int64_t panels) { return (panels + 7) / 8 * 8; }
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Cost of a plan in cycles (tile_gemm.hip's, on this kernel's steps).
@@ -340,17 +369,16 @@ TilePlan plan_mx(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
 
 struct Layout {
     TilePlan plan;
-    int64_t w_panels, w_pad, x_pad, groups, x_at, part_at, total;
+    int64_t w_panels, groups, part_at, total;
+    bool images;               // of the scales
 };
 Layout layout(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
     Layout l{};
     l.plan = plan_mx(x_type, nmat, M, N, K);
     l.w_panels = panels_of(N) * nmat;
-    l.w_pad = padded(l.w_panels);
-    l.x_pad = padded(panels_of(M));
     l.groups = (K + 255) / 256;
-    l.x_at = up256(l.groups * l.w_pad * kScaleUnit);
-    l.part_at = l.x_at + up256(l.groups * l.x_pad * kScaleUnit);
+    l.images = K % 256 != 0;
+    l.part_at = l.images ? up256(l.groups * (N * nmat + M) * 8) : 0;
     l.total = l.part_at + partial_bytes(l.plan, M, l.w_panels);
     return l;
 }
@@ -387,23 +415,24 @@ hipError_t launch_mx_tile(const MxLinearArgs& p, const EpilogueArgs& epi, void* 
     }
     a.xq = static_cast<const uint8_t*>(l.x);
     a.xs = p.x_s;
-    a.w_scales = reinterpret_cast<uint32_t*>(ws);
-    a.x_scales = reinterpret_cast<uint32_t*>(ws + at.x_at);
     a.part = reinterpret_cast<float*>(ws + at.part_at);
     a.N = l.N;
     a.K = l.K;
     a.w_panels = at.w_panels;
-    a.w_pad = at.w_pad;
-    a.x_pad = at.x_pad;
     a.groups = at.groups;
     a.parts = at.plan.parts;
     a.epi = epi;
-    const int64_t threads = (at.w_pad + at.x_pad) * ((at.groups + 1) / 2) * 32;
+    const int64_t rows = l.N * l.nmat + l.M, threads = at.groups * rows;
+    a.scales = ws;
+    for (int i = 0; i < 2; i++) a.w_scales[i] = at.images ? ws + i * l.N * 8 : a.ws[i];
+    a.x_scales = at.images ? ws + l.N * l.nmat * 8 : a.xs;
+    a.scale_row = (uint32_t)(at.images ? 8 : l.K / 32);
+    a.scale_group = at.images ? rows * 8 : 8;
     const TilePlan& plan = at.plan;
     const int64_t tiles = ((at.w_panels + 2 * plan.nt - 1) / (2 * plan.nt)) *
                           ((panels_of(l.M) + 2 * plan.mt - 1) / (2 * plan.mt)) * plan.parts;
     if (!launchable((threads + 255) / 256, 256) || !launchable(tiles, 256)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(k_mx_scales, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
+    if (at.images) hipLaunchKernelGGL(k_mx_scales, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, a);
     const int which = plan.parts > 1 ? EPI_PARTIAL : l.nmat == 2 ? EPI_GATED : EPI_LINEAR;
     if (p.x_type == XT_MXFP8) launch_type<XT_MXFP8>(plan, which, a, (unsigned)tiles, s);
     else launch_type<XT_MXFP4>(plan, which, a, (unsigned)tiles, s);

@@ -13,11 +13,14 @@ struct MxTileArgs {
     const uint8_t* ws[2];
     const uint8_t* xq;
     const uint8_t* xs;
-    uint32_t* w_scales;        // images (k_mx_scales)
-    uint32_t* x_scales;
     int64_t N, K;
-    int64_t w_panels, w_pad, x_pad;      // panels of W (gate and up in turn), and of the scale images
+    int64_t w_panels;          // of W: gate and up in turn
     int64_t groups;            // of 256 k
+    uint8_t* scales;           // images of the scales, or null
+    const uint8_t* w_scales[2];          // a row's eight bytes of group t: + row * scale_row + t * scale_group
+    const uint8_t* x_scales;
+    uint32_t scale_row;
+    int64_t scale_group;
     float* part;
     EpilogueArgs epi;
 };
