@@ -9,7 +9,7 @@
 //
 // A workgroup of four waves owns a tile of 2 NT x 2 MT panels of 32 (columns x
 // rows), each wave NT x MT of them.  The sum runs in steps of 128 k through a ring
-// of three LDS slots that direct-to-LDS copies fill from the planes: a copy is 16
+// of LDS slots (mx_ring) that direct-to-LDS copies fill from the planes: a copy is 16
 // rows by 64 bytes (8 rows by 128 at 8 bits), so that four (eight) neighbouring
 // lanes read whole lines, and the 16-byte pieces of a row are placed by an XOR with
 // the row, so that the reads of an operand, 32 rows apart by a row's pitch, meet no
@@ -26,7 +26,6 @@ namespace q4 {
 
 namespace {
 
-constexpr int kRing = 3;
 constexpr int kScaleUnit = 256;            // bytes of a panel's scales for 256 k
 
 // copy_unit for four bytes a lane.
@@ -67,6 +66,16 @@ __global__ __launch_bounds__(256) void k_mx_scales(const MxTileArgs a) {
 
 // ---- the product -------------------------------------------------------------------
 
+// Slots of the ring: what LDS holds, six at most -- from a copy to its use lie kRing - 1
+// steps, 1400 cycles each at 4 x 2 panels, and memory may take two of them.  2 x 2
+// panels take half of LDS, so that two workgroups share a CU.
+template <int NT, int MT>
+constexpr int mx_ring(int slot, int scale_slot) {
+    const int lds = (NT * MT == 4 ? 80 : 160) * 1024;
+    for (int r = 6; r > 3; r--)
+        if (r * slot + (r / 2 + 1) * scale_slot <= lds) return r;
+    return 3;
+}
 template <int NT, int MT, int EPI>
 constexpr int wave_lds() {
     if constexpr (EPI == EPI_GATED) return 0;
@@ -82,7 +91,8 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
     constexpr int kSlot = 2 * NT * kWPanel + 2 * MT * kXPanel;
     constexpr int kCopies = NT + MT * kXR;                  // of a wave and step, without the scales'
     constexpr int kScaleSlot = 2 * (NT + MT) * kScaleUnit;  // of two steps
-    constexpr int kData = kRing * kSlot, kLoop = kData + 2 * kScaleSlot;
+    constexpr int kRing = mx_ring<NT, MT>(kSlot, kScaleSlot), kScaleRing = kRing / 2 + 1;
+    constexpr int kData = kRing * kSlot, kLoop = kData + kScaleRing * kScaleSlot;
     constexpr int kWaveB = wave_lds<NT, MT, EPI>();          // the epilogue's tiles lie where the operands were
     constexpr int kScaleCopies = (NT + MT) / 2;             // of a wave and two steps
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLoop > 4 * kWaveB ? kLoop : 4 * kWaveB];
@@ -174,7 +184,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
 #pragma unroll
         for (int e = 0; e < kScaleCopies; e++)
             copy_dwords(scalar(s_src[e] + (int64_t)t * a.scale_group), s_at[e],
-                        lds0 + (uint32_t)(kData + (g & 1) * kScaleSlot + (e * 4 + wave) * kScaleUnit));
+                        lds0 + (uint32_t)(kData + g % kScaleRing * kScaleSlot + (e * 4 + wave) * kScaleUnit));
     };
 
     floatx16_t acc[NT][MT];
@@ -214,7 +224,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
     typedef uint64_t scale_t;
     scale_t sc[NT + MT], next_sc[NT + MT];
     auto read_scales = [&](int g, scale_t (&to)[NT + MT]) __attribute__((always_inline)) {
-        const scale_t* p = reinterpret_cast<const scale_t*>(lds + kData + (g & 1) * kScaleSlot);
+        const scale_t* p = reinterpret_cast<const scale_t*>(lds + kData + g % kScaleRing * kScaleSlot);
 #pragma unroll
         for (int i = 0; i < NT; i++) to[i] = p[(wn * NT + i) * 32 + r];
 #pragma unroll
@@ -242,12 +252,15 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
     constexpr int kLate = 2 * kFrags - kEarly;              // the rest, and half 1: read before this step's barrier
     constexpr int kLead = T / 4 < 4 ? T / 4 : 4;            // MFMAs between the last of them and the barrier
     static_assert(B - kLead > 0, "room for the reads");
-    // copies of the step after next but one run from a barrier to the next one's
+    // a step's copies run from a barrier to the next one's
     constexpr int kAfter = (kCopies * (T - B) + T - 1) / T;          // of them before the step's end
 
     auto step = [&](int i, auto odd) __attribute__((always_inline)) {
         constexpr int kOdd = decltype(odd)::value;
-        const int slot = i % kRing, next = (i + 1) % kRing, third = (i + 2) % kRing;
+        const int slot = i % kRing, next = (i + 1) % kRing, before = (i + kRing - 1) % kRing;
+        // the step whose copies end in this one is i + kRing - 1; the scales go with the even ones
+        constexpr bool kScales = (kOdd + kRing - 1) % 2 == 0;
+        constexpr int kAhead = kRing - 2, kAheadScales = (kAhead + (kOdd ? 0 : 1)) / 2;      // in flight at the barrier
         const uint8_t* here = lds + slot * kSlot;
         const uint8_t* there = lds + next * kSlot;
         __builtin_amdgcn_sched_barrier(0);
@@ -255,7 +268,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         for (int q = 0; q < T; q++) {
             if (q == B) {
                 // the next step has landed (and its scales), the one after it is in flight
-                step_barrier<kCopies + (kOdd ? 0 : kScaleCopies)>();
+                step_barrier<kAhead * kCopies + kAheadScales * kScaleCopies>();
                 ahead++;
                 stand();
                 __builtin_amdgcn_sched_barrier(0);
@@ -274,11 +287,11 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
                 if (B + f * (T - B) / kEarly == q) read(f, there, 0, fa);
 #pragma unroll
             for (int t = 0; t < kCopies; t++) {
-                // into the slot just read, for the step after next but one; the rest of the one before
+                // into the slot just read, for step i + kRing; the rest of the one before
                 if (t < kAfter && B + t * (T - B) / kAfter == q) copy(t, slot);
-                if (t >= kAfter && (t - kAfter) * B / (kCopies - kAfter) == q) copy(t, third);
+                if (t >= kAfter && (t - kAfter) * B / (kCopies - kAfter) == q) copy(t, before);
             }
-            if (!kOdd && q == 1) copy_scales((i >> 1) + 1);
+            if (kScales && q == 1) copy_scales((i + kRing - 1) >> 1);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (kOdd) {
@@ -288,8 +301,9 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
     };
 
     if (S > 0) {
-        copy_scales(0);
+#pragma unroll
         for (int p = 0; p < kRing - 1; p++) {
+            if (p % 2 == 0) copy_scales(p / 2);
             stand();
 #pragma unroll
             for (int t = 0; t < kCopies; t++) copy(t, p);
@@ -298,7 +312,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         stand();
 #pragma unroll
         for (int t = 0; t < kAfter; t++) copy(t, kRing - 1);
-        step_barrier<kCopies + kAfter>();
+        step_barrier<(kRing - 2) * kCopies + (kRing - 2) / 2 * kScaleCopies + kAfter>();
         read_scales(0, sc);
 #pragma unroll
         for (int e = 0; e < NT + MT; e++) sc[e] >>= 8 * h;
