@@ -307,37 +307,42 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
         }
     __syncthreads();
     // four columns a thread
-    const int cols = plan.rw * R * kRows, quads = cols / 4, n0 = (int)blockIdx.x * cols;
-    const bool vec = N % 4 == 0;
-    for (int o = threadIdx.x; o < quads * M; o += blockDim.x) {
-        const int m = o / quads, i = o % quads * 4, n = n0 + i, left = N - n;
-        if (left <= 0) continue;
-        const int tile = i / kRows, from = tile / R;          // row tile of the workgroup, its wave row
-        auto sum = [&](int t, float (&z)[4]) __attribute__((always_inline)) {
-            floatx4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int k = 0; k < plan.kw; k++)
-                v += *reinterpret_cast<const floatx4_t*>(red + (((from * plan.kw + k) * R + tile % R) * NM + t) * kTile +
-                                                         m * kPitch + i % kRows);
+    auto finish = [&](auto type) __attribute__((always_inline)) {
+        constexpr int kDt = decltype(type)::value;
+        const int cols = plan.rw * R * kRows, quads = cols / 4, n0 = (int)blockIdx.x * cols;
+        const bool vec = N % 4 == 0;
+        for (int o = threadIdx.x; o < quads * M; o += blockDim.x) {
+            const int m = o / quads, i = o % quads * 4, n = n0 + i, left = N - n;
+            if (left <= 0) continue;
+            const int tile = i / kRows, from = tile / R;          // row tile of the workgroup, its wave row
+            auto sum = [&](int t, float (&z)[4]) __attribute__((always_inline)) {
+                floatx4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int k = 0; k < plan.kw; k++)
+                    v += *reinterpret_cast<const floatx4_t*>(red + (((from * plan.kw + k) * R + tile % R) * NM + t) * kTile +
+                                                             m * kPitch + i % kRows);
 #pragma unroll
-            for (int e = 0; e < 4; e++) z[e] = v[e];
-        };
-        const int64_t at = (int64_t)m * N + n;
-        float z[4], none[4];
-        sum(0, z);
-        if (a.bias[0]) add4(a.bias[0], a.dtype, n, left, vec, z);
-        if (a.pre[0]) put4(a.pre[0], a.dtype, at, left, vec, z);
-        activate_all<false>(a.act, z, z, none);
-        if constexpr (NM == 2) {
-            float u[4];
-            sum(1, u);
-            if (a.bias[1]) add4(a.bias[1], a.dtype, n, left, vec, u);
-            if (a.pre[1]) put4(a.pre[1], a.dtype, at, left, vec, u);
+                for (int e = 0; e < 4; e++) z[e] = v[e];
+            };
+            const int64_t at = (int64_t)m * N + n;
+            float z[4], none[4];
+            sum(0, z);
+            if (a.bias[0]) add4(a.bias[0], kDt, n, left, vec, z);
+            if (a.pre[0]) put4(a.pre[0], kDt, at, left, vec, z);
+            activate_all<false>(a.act, z, z, none);
+            if constexpr (NM == 2) {
+                float u[4];
+                sum(1, u);
+                if (a.bias[1]) add4(a.bias[1], kDt, n, left, vec, u);
+                if (a.pre[1]) put4(a.pre[1], kDt, at, left, vec, u);
 #pragma unroll
-            for (int e = 0; e < 4; e++) z[e] *= u[e];
+                for (int e = 0; e < 4; e++) z[e] *= u[e];
+            }
+            if (a.residual) add4(a.residual, kDt, at, left, vec, z);
+            put4(a.y, kDt, at, left, vec, z);
         }
-        if (a.residual) add4(a.residual, a.dtype, at, left, vec, z);
-        put4(a.y, a.dtype, at, left, vec, z);
-    }
+    };
+    if (XT == DT_BF16 || (XT != DT_F16 && a.dtype == DT_BF16)) finish(std::integral_constant<int, DT_BF16>{});
+    else finish(std::integral_constant<int, DT_F16>{});
 }
 
 // ---- host ------------------------------------------------------------------------

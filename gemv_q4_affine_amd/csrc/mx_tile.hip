@@ -57,10 +57,15 @@ __global__ __launch_bounds__(256) void k_mx_scales(const MxTileArgs a) {
     const int mat = is_w && i >= a.N ? 1 : 0;
     const int64_t row = is_w ? i - mat * a.N : i - a.N * a.nmat;
     const uint8_t* s = (is_w ? a.ws[mat] : a.xs) + row * nb;
+    typedef u32x2_t u32x2_b __attribute__((aligned(1)));
     u32x2_t v = {0u, 0u};
+    if (8 * t + 8 <= nb) {
+        v = *reinterpret_cast<const u32x2_b*>(s + 8 * t);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-        if (8 * t + e < nb) v[e >> 2] |= (uint32_t)s[8 * t + e] << (8 * (e & 3));
+        for (int e = 0; e < 8; e++)
+            if (8 * t + e < nb) v[e >> 2] |= (uint32_t)s[8 * t + e] << (8 * (e & 3));
+    }
     reinterpret_cast<u32x2_t*>(a.scales)[t * all + i] = v;
 }
 
@@ -188,12 +193,6 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
     };
 
     floatx16_t acc[NT][MT];
-#pragma unroll
-    for (int i = 0; i < NT; i++)
-#pragma unroll
-        for (int j = 0; j < MT; j++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
 
     // ---- fragments of 64 k: half kk of a step ----
     const int r = lane & 31, h = lane >> 5;
@@ -300,6 +299,14 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         }
     };
 
+    auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int j = 0; j < MT; j++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+    };
     if (S > 0) {
 #pragma unroll
         for (int p = 0; p < kRing - 1; p++) {
@@ -312,6 +319,7 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
         stand();
 #pragma unroll
         for (int t = 0; t < kAfter; t++) copy(t, kRing - 1);
+        clear();                                             // while the copies travel
         step_barrier<(kRing - 2) * kCopies + (kRing - 2) / 2 * kScaleCopies + kAfter>();
         read_scales(0, sc);
 #pragma unroll
@@ -322,6 +330,8 @@ __global__ __launch_bounds__(256, 1) void k_mx_tile(const MxTileArgs a) {
             step(i, std::integral_constant<int, 0>{});
             step(i + 1, std::integral_constant<int, 1>{});
         }
+    } else {
+        clear();
     }
 
     // every copy has landed and every wave has read its last fragments
