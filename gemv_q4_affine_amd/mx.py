@@ -288,21 +288,30 @@ def block_norm_mx(r, y=None, pre_norm=Q4_NORM_RMS, pre_weight=None, pre_bias=Non
     M, D = r.shape
     if D % 32:
         raise ValueError(f"{D} values a row: not whole blocks of 32")
-    at = _here(r)
+    at, shape = _here(r), (M, D)
     dt = y.dtype if y is not None else (dtype or r.dtype)
     if y is not None:
-        _like(y, "y", (M, D), dt)
-        r_out = _out(r_out, "r_out", (M, D), r.dtype, r, stream)
-    _vectors(D, dt, pre_weight=pre_weight, pre_bias=pre_bias, post_weight=post_weight, post_bias=post_bias)
-    rows = _gate_rows(gate, gate_rows, M)
+        _like(y, "y", shape, dt)
+        r_out = _out(r_out, "r_out", shape, r.dtype, r, stream)
+    if pre_weight is not None:
+        _like(pre_weight, "pre_weight", (D,), dt)
+    if pre_bias is not None or post_weight is not None or post_bias is not None:
+        _vectors(D, dt, pre_bias=pre_bias, post_weight=post_weight, post_bias=post_bias)
+    rows = 1
     if gate is not None:
+        rows = _gate_rows(gate, gate_rows, M)
         _like(gate, "gate", (gate.shape[0], D), dt)
     codes, scales = n if n is not None else (None, None)
-    codes = _out(codes, "codes", (M, D // 2 if n_type == Q4_MXFP4 else D), torch.uint8, r, stream)
-    scales = _out(scales, "scales", (M, D // 32), torch.uint8, r, stream)
-    if stats is None and save_stats:
+    width = D // 2 if n_type == Q4_MXFP4 else D
+    if codes is None and scales is None and stream is None:
+        codes, scales = r.new_empty((M, width), dtype=torch.uint8), r.new_empty((M, D // 32), dtype=torch.uint8)
+    else:
+        codes = _out(codes, "codes", (M, width), torch.uint8, r, stream)
+        scales = _out(scales, "scales", (M, D // 32), torch.uint8, r, stream)
+    if stats is not None:
+        _like(stats, "stats", (M, 4), torch.float32)
+    elif save_stats:
         stats = _new((M, 4), torch.float32, r, stream)
-    _like(stats, "stats", (M, 4), torch.float32)
     _check("block_norm_mx",
            lib().block_norm_mx(_p(y, at), _p(r, at), _code(dt), _dt(r), M, D, post_norm, _p(post_weight, at), _p(post_bias, at),
                                _p(gate, at), rows, scale, pre_norm, _p(pre_weight, at), _p(pre_bias, at), eps, _p(r_out, at),
