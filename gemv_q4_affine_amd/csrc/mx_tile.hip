@@ -362,15 +362,18 @@ namespace {
 int64_t panels_of(int64_t rows) { return (rows + 31) / 32; }
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Cost of a plan in cycles (tile_gemm.hip's, on this kernel's steps).
+// Cost of a plan in cycles: rounds of workgroups over the CUs, each a start and an
+// end and its steps, as measured (8-bit x: 4 x 4 panels 2450 a step, of which 2048 its
+// MFMAs; 4-bit x: 1880 of which 1024, bound by the instructions beside them).
 double plan_cost(int nt, int mt, int parts, bool k8, int64_t w_panels, int64_t x_panels, int64_t steps, int cus) {
     const int64_t tiles = ((w_panels + 2 * nt - 1) / (2 * nt)) * ((x_panels + 2 * mt - 1) / (2 * mt));
     const int64_t rounds = (tiles * parts + cus - 1) / cus;
-    const double mfma = 2.0 * (k8 ? 64.0 : 32.0) * nt * mt, lds = 96.0 * (nt + (k8 ? 2 : 1) * mt);
-    const double step = (mfma > lds ? mfma : lds) + 100.0;
-    const double one = 5000.0 + step * (double)((steps + parts - 1) / parts);
+    const int size = nt * mt;                                // 16, 8 or 4
+    const double ends = size == 16 ? 22000.0 : size == 8 ? 15000.0 : 9000.0;
+    const double step = size == 16 ? (k8 ? 2450.0 : 1880.0) : size == 8 ? (k8 ? 1450.0 : 1300.0) : (k8 ? 800.0 : 700.0);
+    // the parts' sums travel to memory and back, and a join is a launch more
     const double join = parts > 1 ? 6000.0 + 8.0 * parts * (double)(x_panels * w_panels) * 1024.0 / 2000.0 : 0.0;
-    return rounds * one + join;
+    return rounds * (ends + step * (double)((steps + parts - 1) / parts)) + join;
 }
 
 TilePlan plan_mx(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
