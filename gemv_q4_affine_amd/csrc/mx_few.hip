@@ -360,6 +360,7 @@ MxFewPlan plan_few(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 
+// (at most 2^25 / 12 workgroups of 512: far below a launch's 2^32 threads)
 template <int XT, int P, int MT, int NM, int R>
 void launch(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
     const int64_t cols = (int64_t)p.rw * R * (16 / P);
