@@ -158,6 +158,7 @@ static EpilogueArgs epilogue_args(const LinearArgs& a) {
 
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
     if (a.M <= kFewCallMaxM) {
+        if (a.wf == WF_MXFP4) return hipErrorInvalidValue;   // those rows are launch_mx_few's
         const int64_t first = few_rows_of(a.M);
         const FewPlan p = plan_few(a.wf, a.nmat, first, a.N, a.K);
         float* part = static_cast<float*>(workspace);
