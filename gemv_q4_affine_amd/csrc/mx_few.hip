@@ -15,9 +15,17 @@
 // rows by 256 contiguous bytes, and of the 16 x 16 sums those with p = q count,
 // four lanes' worth added up at the end.  Above four rows P is 1.
 //
-// A wave takes groups of four such chunks, 64 P^-1 .. k, of R row tiles; the waves of a
-// workgroup split the sum (KW of them) and the rows, and add their sums through
-// LDS in wave order.  Scales: one 16-byte load a tile and group.
+// A wave takes groups of four such chunks (64 blocks a row at P = 4, else 16) of R row
+// tiles, all of a group's loads before its first product; the waves of a workgroup
+// split the sum (KW of them) and the rows, and add their sums through LDS in wave
+// order.  Scales: one 16-byte load a tile and group.  Above four rows x comes by
+// direct copies to LDS, a wave's own part of it.
+//
+// Bounds.  One row: memory, and the round trip of a short launch: a pair of 12288 x 4096
+// in 11.5 us (57 MB, 4.9 TB/s; a large copy reaches 5.2), one in 7.3, one 32768 x 4096 in
+// 13.6 (5.2 TB/s), one 2048 x 8192 with bfloat16 x in 4.9.  5 to 64 rows: every workgroup
+// reads all of x through LDS (12288 x 4096 with 8-bit x: 16 rows 8.5, 32 9.6, 64 13.0 us);
+// 16-bit x also the conversions beside the products (12.2 us at 32 rows; binary16 twice the products).
 #include "gemm_common.hpp"
 #include "mx_few.hpp"
 #include "tile_image.hpp"
@@ -349,14 +357,29 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
 
 namespace {
 
-MxFewPlan plan_few(int64_t M, int64_t N, int64_t K) {
+// Waves along the sum first, as many as it has groups.  (16 x 12288 x 4096 with 8-bit x: 8.5 us
+// with eight of them, 11.1 with four and two along the rows; up to four rows no difference.)
+// Then one to three row tiles a wave, so that the busiest CU has the fewest of them to do, and
+// of equals the most: a wave then has more loads in flight, and a fragment of x serves more
+// products.  us with one, two and three tiles, 8-bit x but where said:
+//   1 x 4096 x 4096   3.5  4.0  4.3     1 x 12288 x 4096         7.8   7.1   7.3
+//   1 x 8192 x 4096   6.3  5.4  6.4     1 x 12288 x 4096 gated   12.4  12.7  11.5
+//   16 x 12288 x 4096 9.9  9.9  8.6     1 x 12288 x 4096 binary16 17.6 15.6  12.9
+//   16 x 32768 x 4096 19.9 16.4 17.0    4 x 32768 x 4096 bfloat16 25.7 17.6  19.9
+MxFewPlan plan_few(int nmat, int64_t M, int64_t N, int64_t K) {
     const int P = M <= 4 ? 4 : 1;
-    const int64_t groups = (K / 32 + 16 * P - 1) / (16 * P), tiles = (N + 16 / P - 1) / (16 / P);
+    const int64_t groups = (K / 32 + 16 * P - 1) / (16 * P), tiles = (N + 16 / P - 1) / (16 / P), cus = current_cu_count();
     MxFewPlan p{};
     p.kw = (int)(groups < 8 ? groups : 8);
     p.rw = 8 / p.kw;
-    const int64_t per = tiles / ((int64_t)p.rw * current_cu_count());
-    p.r = per <= 1 ? 1 : per == 2 ? 2 : 3;
+    int64_t least = 0;
+    for (int r = nmat == 2 && M > 32 ? 1 : 3; r >= 1; r--) { // (the registers hold no more than one there)
+        const int64_t workgroups = (tiles + p.rw * r - 1) / (p.rw * r), of_cu = (workgroups + cus - 1) / cus * r;
+        if (least == 0 || of_cu < least) {
+            least = of_cu;
+            p.r = r;
+        }
+    }
     return p;
 }
 
@@ -368,7 +391,7 @@ void launch(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
 }
 template <int XT, int P, int MT, int NM>
 void launch_r(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
-    if constexpr (P == 4 || MT * NM < 8) {
+    if constexpr (MT * NM < 8) {
         if (p.r == 2) return launch<XT, P, MT, NM, 2>(a, p, s);
         if (p.r == 3) return launch<XT, P, MT, NM, 3>(a, p, s);
     }
@@ -389,8 +412,19 @@ void launch_x(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
 
 }  // namespace
 
+// Up to 64 rows (64 x 12288 x 4096 with 8-bit x: 13.0 us here, 18.9 as tiles; 64 x 4096 x 12288:
+// 18.4 and 18.9).  Gated and above 32 rows a wave has one row tile, and where that makes more
+// than one round of workgroups the tiles are faster (64 x 4096 x 4096: 11.4 here, 17.1 as tiles;
+// 64 x 12288 x 4096: 28.3 and 22.5).
+bool mx_few_takes(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
+    if (M > 64) return false;
+    if (nmat == 1 || M <= 32 || (x_type != XT_MXFP8 && x_type != XT_MXFP4)) return true;
+    const MxFewPlan p = plan_few(nmat, M, N, K);
+    return (N + 16 * p.rw - 1) / (16 * p.rw) <= (int64_t)current_cu_count();
+}
+
 hipError_t launch_mx_few(const MxLinearArgs& a, hipStream_t s) {
-    const MxFewPlan p = plan_few(a.a.M, a.a.N, a.a.K);
+    const MxFewPlan p = plan_few(a.a.nmat, a.a.M, a.a.N, a.a.K);
     if (a.x_type == XT_MXFP8) launch_x<XT_MXFP8>(a, p, s);
     else if (a.x_type == XT_MXFP4) launch_x<XT_MXFP4>(a, p, s);
     else if (a.x_type == DT_BF16) launch_x<DT_BF16>(a, p, s);

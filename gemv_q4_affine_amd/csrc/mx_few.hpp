@@ -5,7 +5,9 @@
 
 namespace q4 {
 
-constexpr int64_t kMxFewMaxM = 64;
+// Whether a product goes to launch_mx_few, else to the tile products (mx_tile.hip,
+// linear.hip: 16-bit x there must have more than 64 rows).
+bool mx_few_takes(int x_type, int nmat, int64_t M, int64_t N, int64_t K);
 
 // Waves of a workgroup along the sum and along the rows of W, row tiles of a wave.
 struct MxFewPlan {

@@ -139,3 +139,20 @@ def test_refused_tensors():
         Q.mx_linear(w, planes(100, 96, 8, 2), workspace=None)                  # needs one
     with pytest.raises(TypeError):
         Q.mx_linear(w, torch.zeros(5, 96, device="cuda", dtype=torch.float64))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,N,K", [(33, 12290, 4128), (50, 9000, 2048), (64, 5000, 4096), (64, 4096, 4096), (40, 70000, 64), (32, 12290, 4128)])
+def test_gated_by_columns_or_tiles(M, N, K, bits):
+    """33 to 64 rows: where the row tiles make one round of the GPU they are streamed, else multiplied as tiles."""
+    kind = "fp8" if bits == 8 else "fp4"
+    w, u, x = planes(N, K, 4, M), planes(N, K, 4, M + 1), planes(M, K, bits, N)
+    h, g, up = Q.mx_gated(w, u, x, save_pre=True)
+    g64, u64 = values(x) @ values(w).T, values(x) @ values(u).T
+    h64 = act64(g64, "silu") * u64
+    grow = max(1.0, 1.13 * ((g64.abs() * u64.abs()).norm() / h64.norm()).item())
+    near(h, h64.cpu(), U[torch.bfloat16] + 2.0 * grow * (bar(torch.bfloat16, kind) - U[torch.bfloat16]), "h")
+    near(g, g64.cpu(), bar(torch.bfloat16, kind), "g")
+    near(up, u64.cpu(), bar(torch.bfloat16, kind), "u")
+    for m in (0, M - 1):                                     # rows do not depend on their neighbours
+        assert torch.allclose(Q.mx_linear(w, (x[0][m:m + 1].clone(), x[1][m:m + 1].clone())).float(), g[m].float(), rtol=2.0 ** -6, atol=1e-4 * g64.abs().max().item())
