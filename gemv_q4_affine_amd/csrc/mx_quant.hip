@@ -2,8 +2,12 @@
 //
 // A lane takes eight consecutive values, four lanes a block of 32: the block's
 // largest |value| is the maximum of the magnitudes' bit patterns (which also
-// orders infinities and NaNs above every number) over the quad.  Bound by
-// memory: one read and one write of each value.
+// orders infinities and NaNs above every number) over the quad.  Eight values a
+// lane make a wave's reads and writes whole lines in both directions, and the
+// conversions are the hardware's, four instructions a lane.  Bound by memory, one read
+// and one write of each value: 12288 x 4096 bfloat16 to 4 bits 19.6 us and back
+// 19.4 (127 MB, 6.5 TB/s, part of it from the last-level cache; a large copy moves 5.2),
+// 1001 x 8192 to 8 bits 5.0 (25 MB).
 #include "mx_common.hpp"
 #include "tile_image.hpp"
 
