@@ -173,12 +173,39 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
                                [&](int64_t m) __attribute__((always_inline)) { return ldexpf(1.0f, -(int)a.xexp[m]); });
 }
 
+// Sixteen columns of the sums of row groups by 256 threads, in k_join_sums's order:
+// sixteen ranges of the groups, then the ranges.
+__device__ __forceinline__ void join_sums16(const SumsArgs& a, unsigned block) {
+    __shared__ float red[16][16];
+    const unsigned across = (unsigned)((a.N + 15) / 16);
+    const int i = (int)(block / across), col = threadIdx.x & 15, range = threadIdx.x >> 4;
+    const int64_t n = (int64_t)(block % across) * 16 + col;
+    float* out = a.out[i];
+    if (!out) return;
+    const int64_t last = a.groups * (range + 1) / 16;
+    float t = 0.0f;
+    if (n < a.N)
+#pragma unroll 8
+        for (int64_t g = a.groups * range / 16; g < last; g++) t += a.sums[(g * a.nmat + i) * a.N + n];
+    red[range][col] = t;
+    __syncthreads();
+    if (range == 0 && n < a.N) {
+        for (int w = 1; w < 16; w++) t += red[w][col];
+        out[n] = t;
+    }
+}
+
 // The parts of a split sum joined in order and scaled, then the epilogue: one
-// thread for eight columns of a row.
+// thread for eight columns of a row.  The first `sum_blocks` workgroups join the
+// bias gradients.
 template <int EPI>
-__global__ __launch_bounds__(256) void k_tile_join(const TileArgs a) {
+__global__ __launch_bounds__(256) void k_tile_join(const TileArgs a, const unsigned sum_blocks) {
+    if (blockIdx.x < sum_blocks) {
+        join_sums16(a.sums, blockIdx.x);
+        return;
+    }
     const int64_t chunks = (a.epi.N + 7) / 8;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = (int64_t)(blockIdx.x - sum_blocks) * 256 + threadIdx.x;
     if (id >= a.epi.M * chunks) return;
     const int64_t m = id / chunks, n = id % chunks * 8, np = a.w_panels * 32;
     const int64_t at = EPI == EPI_GATED ? n / 32 * 64 + n % 32 : n;
@@ -252,10 +279,11 @@ static void launch_shape(int epi, const TileArgs& a, unsigned grid, hipStream_t 
 
 hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s) {
     const int64_t threads = a.epi.M * ((a.epi.N + 7) / 8);
-    if (!launchable((threads + 255) / 256, 256)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)((threads + 255) / 256));
-    if (nmat == 2) hipLaunchKernelGGL((k_tile_join<EPI_GATED>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_tile_join<EPI_LINEAR>), grid, dim3(256), 0, s, a);
+    const int64_t sum_blocks = (a.sums.N + 15) / 16 * a.sums.nmat, blocks = sum_blocks + (threads + 255) / 256;
+    if (!launchable(blocks, 256)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks);
+    if (nmat == 2) hipLaunchKernelGGL((k_tile_join<EPI_GATED>), grid, dim3(256), 0, s, a, (unsigned)sum_blocks);
+    else hipLaunchKernelGGL((k_tile_join<EPI_LINEAR>), grid, dim3(256), 0, s, a, (unsigned)sum_blocks);
     return hipGetLastError();
 }
 

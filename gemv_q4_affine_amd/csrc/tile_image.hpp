@@ -43,6 +43,15 @@ struct EpilogueArgs {
     void* pre[2];
 };
 
+// The bias gradients: sums over groups of rows, [groups][nmat][N], joined in order
+// into the columns of out (null: none).
+struct SumsArgs {
+    const float* sums;
+    int64_t groups, N;
+    int nmat;
+    float* out[2];
+};
+
 // One product Z[m][n] = sum_k X[m][k] W[n][k] over two images.
 struct TileArgs {
     const uint8_t* wimg;
@@ -54,6 +63,7 @@ struct TileArgs {
     float* part;               // [parts][M][N'] sums as they were added up, N' = w_panels * 32
     float unit;                // of them where there is no xexp
     EpilogueArgs epi;
+    SumsArgs sums;             // nmat 0: none; joined with the parts
 };
 
 // The plan of a product: tile shape (panels of a wave: a workgroup's tile is
@@ -78,6 +88,9 @@ hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool tw
 // dz of every projection: the image, the dz outputs and the column sums.
 int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N);
 hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s);
+// What launch_pack_dz leaves in `sums` to be joined, by launch_join_sums or with a split product's parts.
+SumsArgs sums_args(const LinearGradArgs& a, const float* sums);
+hipError_t launch_join_sums(const SumsArgs& a, hipStream_t s);
 
 // ---- eight values at a time ----------------------------------------------------
 

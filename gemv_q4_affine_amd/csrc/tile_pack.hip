@@ -351,7 +351,7 @@ hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool tw
 
 // dz of the projections: the same image (the projections' slices follow each
 // other), the dz outputs rounded from the same binary32 values, and the sums of
-// the workgroup's rows, joined by k_join_sums in a fixed order.
+// the workgroup's rows, joined by k_join_sums (or with a split product's parts) in a fixed order.
 template <bool VEC>
 __device__ __forceinline__ void load_dz(const LinearGradArgs& a, int64_t o, int left, float (&dz)[2][8]) {
     unpack8(DT_BF16, load8_raw<VEC>(a.dy, o, left), dz[0]);
@@ -482,7 +482,7 @@ int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N) { return (M + pack_rows(
 
 hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s) {
     const int rows = pack_rows(a.M);
-    const int64_t groups = (a.M + rows - 1) / rows, slices = image_slices(a.N);
+    const int64_t slices = image_slices(a.N);
     auto k = a.N % 8 == 0 ? (rows == 8 ? k_pack_dz<true, 8> : k_pack_dz<true, 4>)
                           : (rows == 8 ? k_pack_dz<false, 8> : k_pack_dz<false, 4>);
     for (int64_t m = 0; m < a.M; m += kLaunchRows) {
@@ -497,9 +497,25 @@ hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, f
         hipLaunchKernelGGL(k, dim3((unsigned)((t.M + rows - 1) / rows)), dim3(kPackThreads), 0, s, t, slices,
                            img + m / 32 * slices * a.nmat * kUnit, xexp + m, sums + m / rows * a.nmat * a.N);
     }
-    if (a.dbias[0] || a.dbias[1])
-        hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(1024), 0, s, sums, groups, a.nmat,
-                           a.N, a.dbias[0], a.dbias[1]);
+    return hipGetLastError();
+}
+
+SumsArgs sums_args(const LinearGradArgs& a, const float* sums) {
+    const int rows = pack_rows(a.M);
+    SumsArgs t{};
+    t.sums = sums;
+    t.groups = (a.M + rows - 1) / rows;
+    t.N = a.N;
+    t.nmat = a.dbias[0] || a.dbias[1] ? a.nmat : 0;
+    t.out[0] = a.dbias[0];
+    t.out[1] = a.dbias[1];
+    return t;
+}
+
+hipError_t launch_join_sums(const SumsArgs& a, hipStream_t s) {
+    if (a.nmat == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_join_sums, dim3((unsigned)((a.N + 63) / 64), a.nmat), dim3(1024), 0, s, a.sums, a.groups, a.nmat, a.N,
+                       a.out[0], a.out[1]);
     return hipGetLastError();
 }
 
