@@ -156,3 +156,16 @@ def test_gated_by_columns_or_tiles(M, N, K, bits):
     near(up, u64.cpu(), bar(torch.bfloat16, kind), "u")
     for m in (0, M - 1):                                     # rows do not depend on their neighbours
         assert torch.allclose(Q.mx_linear(w, (x[0][m:m + 1].clone(), x[1][m:m + 1].clone())).float(), g[m].float(), rtol=2.0 ** -6, atol=1e-4 * g64.abs().max().item())
+
+
+@pytest.mark.parametrize("scale", [104, 140])
+def test_smallest_and_largest_scales_of_the_images(scale):
+    """2^-23 to 2^13: every 4-bit code is exact in binary16, forward and transposed."""
+    M, N, K = 70, 96, 256
+    w = planes(N, K, 4, 7)
+    w[1].fill_(scale)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+    near(Q.mx_linear(w, x), (x.double() @ values(w).T).cpu(), bar(torch.bfloat16), "y")
+    dy = torch.randn(M, N, generator=gen, device="cuda").bfloat16()
+    near(Q.mx_linear_backward(w, dy)["dx"], (dy.double() @ values(w)).cpu(), bar(torch.bfloat16), "dx")
