@@ -18,7 +18,7 @@
 // A wave takes groups of four such chunks (64 blocks a row at P = 4, else 16) of R row
 // tiles, all of a group's loads before its first product; the waves of a workgroup
 // split the sum (KW of them) and the rows, and add their sums through LDS in wave
-// order.  Scales: one 16-byte load a tile and group.  Above four rows x comes by
+// order.  Of more than 64 rows a row of workgroups takes 64 each.  Scales: one 16-byte load a tile and group.  Above four rows x comes by
 // direct copies to LDS, a wave's own part of it.
 //
 // Bounds.  One row: memory, and the round trip of a short launch: a pair of 12288 x 4096
@@ -115,7 +115,9 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kw = wave % plan.kw, rw = wave / plan.kw;
     const int j = lane & 15, g = lane >> 4, p = j & (P - 1);
-    const int K = (int)a.K, N = (int)a.N, M = (int)a.M, nb = K / 32;
+    // above 64 rows a row of workgroups for each 64 of them
+    const int64_t m_first = MT == 4 ? (int64_t)blockIdx.y * 64 : 0;
+    const int K = (int)a.K, N = (int)a.N, nb = K / 32, M = (int)(MT == 4 && a.M - m_first > 64 ? 64 : a.M - m_first);
     const int n_first = ((int)blockIdx.x * plan.rw + rw) * R * kRows;
 
     const uint8_t* wq[R][NM];
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
 #pragma unroll
         for (int i = 0; i < MT; i++) {
             const int first = i * 16 < M ? i * 16 : M - 1;
-            const uint8_t* src = static_cast<const uint8_t*>(a.x) + (int64_t)first * row_x;
+            const uint8_t* src = static_cast<const uint8_t*>(a.x) + (m_first + first) * row_x;
 #pragma unroll
             for (int h = 0; h < 16 / kCopyRows; h++) {
                 const int r = h * kCopyRows + lane / kPieces, in = M - 1 - first;
@@ -200,7 +202,7 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
         if constexpr (kMx) {
 #pragma unroll
             for (int i = 0; i < MT; i++) {
-                xs[i] = scales16(args.x_s + (int64_t)xm[i] * nb, b0 + (P == 4 ? 16 * g : 0), nb);
+                xs[i] = scales16(args.x_s + (m_first + xm[i]) * nb, b0 + (P == 4 ? 16 * g : 0), nb);
                 place(xs[i]);
             }
         }
@@ -331,7 +333,7 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
 #pragma unroll
                 for (int e = 0; e < 4; e++) z[e] = v[e];
             };
-            const int64_t at = (int64_t)m * N + n;
+            const int64_t at = (m_first + m) * N + n;
             float z[4], none[4];
             sum(0, z);
             if (a.bias[0]) add4(a.bias[0], kDt, n, left, vec, z);
@@ -372,9 +374,10 @@ MxFewPlan plan_few(int nmat, int64_t M, int64_t N, int64_t K) {
     MxFewPlan p{};
     p.kw = (int)(groups < 8 ? groups : 8);
     p.rw = 8 / p.kw;
+    const int64_t chunks = (M + 63) / 64;
     int64_t least = 0;
     for (int r = nmat == 2 && M > 32 ? 1 : 3; r >= 1; r--) { // (the registers hold no more than one there)
-        const int64_t workgroups = (tiles + p.rw * r - 1) / (p.rw * r), of_cu = (workgroups + cus - 1) / cus * r;
+        const int64_t workgroups = (tiles + p.rw * r - 1) / (p.rw * r), of_cu = (workgroups * chunks + cus - 1) / cus * r;
         if (least == 0 || of_cu < least) {
             least = of_cu;
             p.r = r;
@@ -387,7 +390,7 @@ MxFewPlan plan_few(int nmat, int64_t M, int64_t N, int64_t K) {
 template <int XT, int P, int MT, int NM, int R>
 void launch(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
     const int64_t cols = (int64_t)p.rw * R * (16 / P);
-    hipLaunchKernelGGL((k_mx_few<XT, P, MT, NM, R>), dim3((unsigned)((a.a.N + cols - 1) / cols)), dim3(64 * p.kw * p.rw), 0, s, a, p);
+    hipLaunchKernelGGL((k_mx_few<XT, P, MT, NM, R>), dim3((unsigned)((a.a.N + cols - 1) / cols), (unsigned)((a.a.M + 63) / 64)), dim3(64 * p.kw * p.rw), 0, s, a, p);
 }
 template <int XT, int P, int MT, int NM>
 void launch_r(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
@@ -416,11 +419,23 @@ void launch_x(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
 // 18.4 and 18.9).  Gated and above 32 rows a wave has one row tile, and where that makes more
 // than one round of workgroups the tiles are faster (64 x 4096 x 4096: 11.4 here, 17.1 as tiles;
 // 64 x 12288 x 4096: 28.3 and 22.5).
+//
+// Above 64 rows 64 at a time in one launch, by the turns (row tiles and groups) of the busiest CU's waves.
+// bfloat16 x, whose other route makes images: to 128 rows, and where there are four turns at most
+// (128 x 12288 x 4096 30.1 us here, 50.3 there; gated 65.0, 91.2; 256 x 4096 x 4096, four turns, 22.9, 33.4;
+// 256 x 6176 x 1280, four, 23.4, 27.4; 512 x 4096 x 4096, eight, 42.4, 40.9; 512 x 6176 x 1280, eight,
+// 51.6, 28.8).  binary16 x takes twice the products: never (128 x 2048 x 8192 36.8, 31.7).
+// MX x: long sums of at most two turns (128 x 4096 x 4096 9.5, as tiles 15.8; 128 x 2048 x 8192 12.8, 17.0;
+// but 128 x 6176 x 1280 11.8, 7.6, and gated 128 x 4096 x 4096 20.0, 19.4).
 bool mx_few_takes(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
-    if (M > 64) return false;
-    if (nmat == 1 || M <= 32 || (x_type != XT_MXFP8 && x_type != XT_MXFP4)) return true;
+    const bool mx = x_type == XT_MXFP8 || x_type == XT_MXFP4;
+    if (M <= 64 && (nmat == 1 || M <= 32 || !mx)) return true;
+    if (M > 64 && !(mx ? nmat == 1 && K >= 4096 : x_type == DT_BF16)) return false;
     const MxFewPlan p = plan_few(nmat, M, N, K);
-    return (N + 16 * p.rw - 1) / (16 * p.rw) <= (int64_t)current_cu_count();
+    const int64_t cus = current_cu_count(), cols = (int64_t)16 * p.rw * p.r, workgroups = (N + cols - 1) / cols * ((M + 63) / 64);
+    if (M <= 64) return workgroups <= cus;
+    const int64_t groups = (K / 32 + 15) / 16, turns = (workgroups + cus - 1) / cus * p.r * ((groups + p.kw - 1) / p.kw);
+    return mx ? turns <= 2 : M <= 128 || turns <= 4;
 }
 
 hipError_t launch_mx_few(const MxLinearArgs& a, hipStream_t s) {

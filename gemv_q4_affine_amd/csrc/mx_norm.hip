@@ -279,6 +279,8 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
     }
 }
 
+// 1280 threads a CU, a workgroup's rows in turn: 2048 x 4096 17.9 us, with 2560 threads 18.7, a
+// workgroup a row 20.0 (2907 x 672: 9.1, 9.0, 9.0; 3000 x 2048: 16.1, 15.3, 15.4).
 template <int DT, int RT, int V>
 static void norm_v(const MxNormArgs& a, hipStream_t s) {
     const int64_t D = a.norm.D, M = a.norm.M;

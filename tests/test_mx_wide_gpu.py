@@ -169,3 +169,38 @@ def test_smallest_and_largest_scales_of_the_images(scale):
     near(Q.mx_linear(w, x), (x.double() @ values(w).T).cpu(), bar(torch.bfloat16), "y")
     dy = torch.randn(M, N, generator=gen, device="cuda").bfloat16()
     near(Q.mx_linear_backward(w, dy)["dx"], (dy.double() @ values(w)).cpu(), bar(torch.bfloat16), "dx")
+
+
+@pytest.mark.parametrize("M,N,K", [(65, 200, 4128), (128, 3000, 1056), (129, 9000, 2048), (300, 9001, 320), (700, 8200, 544), (1000, 30, 96)])
+def test_bf16_by_columns_or_images(M, N, K):
+    """More than 64 rows of bfloat16: 64 at a time where that is few turns, else images; the residual in place."""
+    w, u = planes(N, K, 4, M), planes(N, K, 4, M + 1)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    x = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+    r = torch.randn(M, N, generator=gen, device="cuda").bfloat16()
+    b = torch.randn(N, generator=gen, device="cuda").bfloat16()
+    z = x.double() @ values(w).T + b.double()
+    y, r64 = r.clone(), r.double()
+    got = Q.mx_linear(w, x, bias=b, residual=y, y=y, save_pre=True)
+    near(y, (z + r64).cpu(), bar(torch.bfloat16), "y")
+    near(got[1], z.cpu(), bar(torch.bfloat16), "pre")
+    h, g, up = Q.mx_gated(w, u, x, save_pre=True)
+    g64, u64 = x.double() @ values(w).T, x.double() @ values(u).T
+    h64 = act64(g64, "silu") * u64
+    grow = max(1.0, 1.13 * ((g64.abs() * u64.abs()).norm() / h64.norm()).item())
+    near(h, h64.cpu(), U[torch.bfloat16] + 2.0 * grow * (bar(torch.bfloat16) - U[torch.bfloat16]), "h")
+    near(g, g64.cpu(), bar(torch.bfloat16), "g")
+    near(up, u64.cpu(), bar(torch.bfloat16), "u")
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("M,N,K", [(65, 4096, 4128), (128, 4000, 4096), (200, 500, 8192), (1000, 20, 4096), (129, 5000, 4096)])
+def test_long_sums_of_a_few_more_rows(bits, M, N, K):
+    kind = "fp8" if bits == 8 else "fp4"
+    w, x = planes(N, K, 4, M), planes(M, K, bits, N)
+    r = torch.randn(M, N, device="cuda").bfloat16()
+    y = r.clone()
+    z = values(x) @ values(w).T
+    got = Q.mx_linear(w, x, residual=y, y=y, save_pre=True)
+    near(got[0], (z + r.double()).cpu(), bar(torch.bfloat16, kind), "y")
+    near(got[1], z.cpu(), bar(torch.bfloat16, kind), "pre")
