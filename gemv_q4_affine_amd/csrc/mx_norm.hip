@@ -247,16 +247,19 @@ __global__ __launch_bounds__(1024) void k_block_norm_mx(const MxNormArgs args) {
                 for (int e = 0; e < 8; e++) t[e] += (double)value<DT>(b, e);
             }
             // Two roundings differ from one only where the first gives a border between
-            // two codes or a power of two: a number whose last 19 bits are zeros.
-            float n[8];
+            // two codes or a power of two.  A normal number that is one ends in 19 zeros;
+            // below 2^-126, where steps are even, borders may end in 12, but only under
+            // scales below 2^-120 and so among values below 2^-112.
+            float n[8], most = 0.0f;
             uint32_t low = ~0u;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 n[e] = (float)t[e];
                 const uint32_t b = __float_as_uint(n[e]) << 13;
                 low = b < low ? b : low;
+                most = fmaxf(most, fabsf(n[e]));
             }
-            if (low == 0u) {
+            if (low == 0u || most < 0x1p-112f) {
 #pragma unroll
                 for (int e = 0; e < 8; e++) n[e] = round_to_odd(t[e]);
             }

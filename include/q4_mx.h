@@ -123,7 +123,8 @@ int mx_gated_backward(const uint8_t* gate_q, const uint8_t* gate_s, const uint8_
  * block_norm_mx -- block_norm (q4_block.h) whose n leaves quantised:
  *   p = post(y);  r' = r + scale * gate * p;  n = pre(r') as codes and scales
  * computed in binary64 from the inputs to the codes, so that these are the ones
- * that mx_quantize's rule gives for the exact n.
+ * that mx_quantize's rule gives for the exact n (one past binary32's range
+ * counts as its largest number).
  *   y .. eps, r_out, stats : as in block_norm, pre_norm not Q4_NORM_NONE
  *             (Q4_ERR_ARG); D % 32 == 0 (Q4_ERR_SHAPE)
  *   n_type    : Q4_MXFP8 or Q4_MXFP4
