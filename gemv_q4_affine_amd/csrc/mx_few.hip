@@ -4,8 +4,8 @@
 //
 // Mathematics.  With MX x a 16x16x128 scaled MFMA takes the codes and scales as
 // they are.  With 16-bit x the codes are converted with their scale to bfloat16,
-// which holds them exactly (2 bits and any scale), and multiplied by bfloat16 x
-// in four 16x16x32 MFMAs; binary16 x is split into two bfloat16 parts, x = hi + lo
+// which holds them exactly (2 bits and any scale up to 2^125; see bf16_scale), and
+// multiplied by bfloat16 x in four 16x16x32 MFMAs; binary16 x is split into two bfloat16 parts, x = hi + lo
 // exactly, and takes eight.  Products are exact, sums binary32.
 //
 // Layout.  Lane l of the MFMA holds one block of 32 of A's row j = l & 15, block
@@ -176,6 +176,7 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
     };
 
     const int groups = (nb + kGroup - 1) / kGroup;
+    bool past = false;                                       // a scale was past bfloat16's range
     for (int kg = kw; kg < groups; kg += plan.kw) {
         const int b0 = kg * kGroup;
         // this lane's block of chunk c, kept inside the row
@@ -279,7 +280,7 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
                     for (int r = 0; r < R; r++)
 #pragma unroll
                         for (int t = 0; t < NM; t++) {
-                            const float s = mx_scale(ws[r][t][c] & 0xFFu);
+                            const float s = bf16_scale(ws[r][t][c] & 0xFFu, past);
                             const uint32_t d = w[r][t][c][e];
                             const u32x4_t q = {bf16_pair<0>(d, s), bf16_pair<1>(d, s), bf16_pair<2>(d, s), bf16_pair<3>(d, s)};
 #pragma unroll
@@ -290,6 +291,46 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
                                     acc[r][t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                                         __builtin_bit_cast(bf16x8_t, q), __builtin_bit_cast(bf16x8_t, lo[i]), acc[r][t][i], 0, 0, 0);
                             }
+                        }
+                }
+            }
+        }
+    }
+
+    // ---- 16-bit x: the blocks past bfloat16's range, as quarters of them four times ----
+    if constexpr (!kMx) {
+        if (__any(past)) {
+#pragma unroll 1
+            for (int slot = kw * 4; slot < groups * 4; slot = (slot & 3) == 3 ? slot + 4 * plan.kw - 3 : slot + 1) {
+                const int b = slot * 4 * P + g * P + p, at = b < nb ? b : nb - 1;     // chunk of a group, its block of this lane
+#pragma unroll 1
+                for (int e = 0; e < 4; e++) {
+                    u32x4_t hi[MT], lo[MT];
+#pragma unroll
+                    for (int i = 0; i < MT; i++) {
+                        u32x4_t v = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + (m_first + xm[i]) * K +
+                                                                      (int64_t)at * 32 + 8 * e);
+                        v = b < nb ? finite16<XT>(v) : u32x4_t{0u, 0u, 0u, 0u};
+                        if constexpr (XT == DT_BF16) hi[i] = v;
+                        else split_f16(v, hi[i], lo[i]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; r++)
+#pragma unroll
+                        for (int t = 0; t < NM; t++) {
+                            const uint32_t s = wsc[r][t][at];
+                            const uint32_t d = *reinterpret_cast<const uint32_t*>(wq[r][t] + (int64_t)at * 16 + 4 * e);
+                            const u32x4_t q = bf16_quarters(past_bf16(s) ? d : 0u, mx_scale(past_bf16(s) ? s : 127u));
+#pragma unroll
+                            for (int i = 0; i < MT; i++)
+#pragma unroll
+                                for (int times = 0; times < 4; times++) {
+                                    acc[r][t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                        __builtin_bit_cast(bf16x8_t, q), __builtin_bit_cast(bf16x8_t, hi[i]), acc[r][t][i], 0, 0, 0);
+                                    if constexpr (XT == DT_F16)
+                                        acc[r][t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                            __builtin_bit_cast(bf16x8_t, q), __builtin_bit_cast(bf16x8_t, lo[i]), acc[r][t][i], 0, 0, 0);
+                                }
                         }
                 }
             }

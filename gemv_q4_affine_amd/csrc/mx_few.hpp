@@ -15,10 +15,42 @@ struct MxFewPlan {
 };
 hipError_t launch_mx_few(const MxLinearArgs& a, hipStream_t s);
 
-// Pair B of the eight 4-bit codes of a word times its scale, in bfloat16 (exact).
+// 16-bit x: W's codes are multiplied in bfloat16, which holds them under every scale up to
+// 2^125; under 2^126 and 2^127 the largest codes are past its range.  Such a block counts as
+// one under 2^-127 (2^-253 of its terms, and what an infinity or a NaN in x makes of them) and
+// sets `past`; its terms are added from quarters of them.
+__device__ __forceinline__ bool past_bf16(uint32_t scale_byte) { return scale_byte == 253u || scale_byte == 254u; }
+__device__ __forceinline__ float bf16_scale(uint32_t s, bool& past) {
+    past |= s >= 253u;                         // (a NaN scale adds nothing there)
+    return __uint_as_float(s - 1u >= 252u ? (s == 255u ? 0x7FC00000u : 0x00400000u) : s << 23);
+}
+// Pair B of the eight 4-bit codes of a word times such a scale, in bfloat16 (exact).
 template <int B>
 __device__ __forceinline__ uint32_t bf16_pair(uint32_t w, float s) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
+}
+
+// The eight codes of a word times a quarter of their scale in bfloat16, exact under any:
+// 2^-130, the least, is a subnormal number of it, and 6 * 2^125 the largest.
+__device__ __forceinline__ u32x4_t bf16_quarters(uint32_t w, float s) {
+    const float f = 0.25f * s;
+    auto pair = [&](f32x2_t v) __attribute__((always_inline)) {
+        const f32x2_t t = {v[0] * f, v[1] * f};
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(t, bf16x2_t));
+    };
+    return u32x4_t{pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)), pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)),
+                   pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)), pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3))};
+}
+
+// 16-bit values with zeros in the place of infinities and NaN.
+template <int DT>
+__device__ __forceinline__ u32x4_t finite16(const u32x4_t& v) {
+    constexpr uint32_t top = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
+    u32x4_t r;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        r[e] = ((v[e] & top) == top ? 0u : v[e] & 0xFFFFu) | ((v[e] >> 16 & top) == top ? 0u : v[e] & 0xFFFF0000u);
+    return r;
 }
 
 // Binary16 values as the sums of two bfloat16 ones: the upper 8 bits, and what

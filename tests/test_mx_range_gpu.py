@@ -83,3 +83,90 @@ def test_norm_past_binary32(kind):
     c64, s64 = X.quantize(n.clip(-top, top), kind)
     _, (codes, scales), _ = Q.block_norm_mx(r.cuda(), pre_weight=w.cuda(), n_type=TYPES[kind])
     assert np.array_equal(scales.cpu().numpy(), s64) and np.array_equal(X.unpacked(codes.cpu().numpy(), kind), c64)
+
+
+# ---- scales ------------------------------------------------------------------------
+
+def weights(scales, seed):
+    """Planes of any codes under the given scale bytes [N, K / 32], and their binary64 values, on the GPU."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    N, K = scales.shape[0], scales.shape[1] * 32
+    q = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    code = torch.stack((q & 15, q >> 4), 2).view(N, K).long()
+    table = torch.from_numpy(X.table("fp4")).cuda()
+    s = torch.exp2(scales.double() - 127).repeat_interleave(32, 1)
+    return (q, scales.to(torch.uint8)), table[code] * s
+
+
+def by_element(got, x, W, what, extra=0.0):
+    """Every output within its own rounding and K + 8 binary32 roundings of the sum of its terms' magnitudes, where those
+    lie inside binary32's normal numbers (and the output inside its type)."""
+    want, terms = x @ W.T, x.abs() @ W.abs().T
+    top = min(float(torch.finfo(got.dtype).max), 2.0 ** 126)
+    inside = (terms < top * 0.99) & (terms > 2.0 ** -100)
+    slack = want.abs() * (torch.finfo(got.dtype).eps / 2) + terms * ((x.shape[1] + 8) * 2.0 ** -24 + extra)
+    if got.dtype == torch.float16:
+        slack += 2.0 ** -25
+    e = ((got.double() - want).abs() / slack)[inside]
+    say(f"  {what}: {inside.double().mean().item():.2f} of the outputs, {e.max().item() if e.numel() else 0:.3g} of the slack")
+    assert torch.isfinite(got[inside]).all() and (e <= 1).all(), what
+    return inside
+
+
+#: 255 rows of W, each under a scale of its own, times `more`; the routes by rows, on 16-bit x.
+ROUTES = [(1, 1, 160), (4, 1, 2080), (5, 1, 160), (20, 1, 544), (40, 1, 8192), (64, 1, 160)]
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("M,more,K", ROUTES)
+def test_every_scale_of_the_weights(x, M, more, K):
+    dt = {"bf16": torch.bfloat16, "f16": torch.float16}[x]
+    w, W = weights(torch.arange(255, device="cuda").repeat(more)[:, None].expand(255 * more, K // 32).contiguous(), M)
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    seen = torch.zeros(255 * more, dtype=torch.bool, device="cuda")
+    for e in (-100, -50, 0, 50, 100) if x == "bf16" else (-13, -6, 0, 6, 12):
+        v = (torch.randn(M, K, generator=gen, device="cuda").clamp(-4, 4) * 2.0 ** e).to(dt)
+        seen |= by_element(Q.mx_linear(w, v), v.double(), W, f"{x} {M} 2^{e}").any(0)
+    assert seen[:255].all() if x == "bf16" else seen[85:135].all()
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("M,more,K", ROUTES)
+def test_blocks_of_very_different_scales(x, M, more, K):
+    """Blocks of W that x's own range balances, so that all of them count: 2^+-100 in bfloat16, 2^+-15 in binary16."""
+    dt, far = {"bf16": (torch.bfloat16, 100), "f16": (torch.float16, 14)}[x]
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    N, nb = 255 * more, K // 32
+    e = torch.tensor([0, far, -far, 3], device="cuda")[torch.arange(nb, device="cuda") % 4]
+    w, W = weights(120 + e + torch.randint(0, 3, (N, nb), generator=gen, device="cuda"), M)
+    v = (torch.randn(M, K, generator=gen, device="cuda") * torch.exp2(-e.double()).repeat_interleave(32)).to(dt)
+    by_element(Q.mx_linear(w, v), v.double(), W, f"{x} {M}")
+
+
+@pytest.mark.parametrize("M", [1, 3, 12, 40, 64])
+def test_largest_scales_and_infinities(M):
+    """Scales of 2^126 and 2^127 beside ordinary ones: an infinity or a NaN in x gives what its terms give, and no other
+    row or column sees it."""
+    K, N = 352, 100
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    s = torch.randint(118, 124, (N, K // 32), generator=gen, device="cuda")
+    s[7::8, 3], s[5::8, 10] = 254, 253
+    w, W = weights(s, M)
+    v = torch.randn(M, K, generator=gen, device="cuda")
+    v[:, 96:128] *= 2.0 ** -110                              # the large blocks' values
+    v[:, 320:] *= 2.0 ** -110
+    v = v.bfloat16()
+    by_element(Q.mx_linear(w, v), v.double(), W, "large")
+    clean = Q.mx_linear(w, v)
+    for k in (5, 100, 340):
+        bad, row = v.clone(), M // 2
+        bad[row, k] = math.inf
+        got = Q.mx_linear(w, bad)
+        others = [m for m in range(M) if m != row]
+        assert torch.equal(got[others], clean[others])
+        col = W[:, k]
+        assert torch.equal(torch.isnan(got[row]), col == 0)
+        assert (got[row][col > 0] == math.inf).all() and (got[row][col < 0] == -math.inf).all()
+        bad[row, k] = math.nan
+        got = Q.mx_linear(w, bad)
+        assert torch.isnan(got[row]).all() and torch.equal(got[others], clean[others])
