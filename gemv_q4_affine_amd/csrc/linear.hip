@@ -19,9 +19,9 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 // exponents, parts of a split sum, column sums.
 struct Layout {
     TilePlan plan;
-    int64_t slices, w_panels, x_panels, x_at, exp_at, part_at, sums_at, total;
+    int64_t slices, w_panels, x_panels, x_at, exp_at, scale_at, part_at, sums_at, total;
 };
-Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M, int64_t sums) {
+Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M, int64_t scales, int64_t sums) {
     Layout l{};
     l.plan = plan;
     l.slices = slices;
@@ -29,16 +29,18 @@ Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M,
     l.x_panels = (M + 31) / 32;
     l.x_at = up256(w_panels * slices * kUnit);
     l.exp_at = l.x_at + l.x_panels * slices * kUnit;
-    l.part_at = l.exp_at + up256(M);
+    l.scale_at = l.exp_at + up256(M);
+    l.part_at = l.scale_at + up256(scales);
     l.sums_at = l.part_at + partial_bytes(plan, M, w_panels);
     l.total = l.sums_at + sums;
     return l;
 }
 // rest: the sum runs over the weights rounded to binary16, then over what the
-// rounding left of them.
-Layout forward_layout(int nmat, bool rest, int64_t M, int64_t N, int64_t K) {
+// rounding left of them.  row_scales: with the scales of the weights' rows.
+Layout forward_layout(int nmat, bool rest, bool row_scales, int64_t M, int64_t N, int64_t K) {
     if (rest) K *= 2;
-    return layout(plan_tiles(nmat, M, N, K), (N + 31) / 32 * nmat, image_slices(K), M, 0);
+    const int64_t w_panels = (N + 31) / 32 * nmat;
+    return layout(plan_tiles(nmat, M, N, K), w_panels, image_slices(K), M, row_scales ? w_panels * 32 : 0, 0);
 }
 // A weight rounded to binary16 puts about as much error into a sum as the
 // rounding of a binary16 output does.  One such error (q4_linear with no
@@ -46,13 +48,22 @@ Layout forward_layout(int nmat, bool rest, int64_t M, int64_t N, int64_t K) {
 // two of a gated product and a curved activation's slope made it 1.6 to 1.8
 // (affine4, 200 rows), so there the remainders are summed too, at twice the matrix
 // work (12288 x 4096, 512 rows, gated: 291 us against 148).  bfloat16 outputs are
-// eight times coarser, and MXFP4 weights are exact in binary16.
+// eight times coarser, and MXFP4 weights are not rounded (form_of).
 bool sums_rest(int wf, int nmat, int dtype, int act) {
     return wf != WF_MXFP4 && dtype == DT_F16 && (nmat == 2 || (act != ACT_NONE && act != ACT_RELU));
 }
+// The image of W.  MXFP4 has two bits under any power of two: against bfloat16 x it goes into
+// bfloat16, which holds both operands as they are, against binary16 x into binary16 under a
+// power of two for each row, which the epilogue takes off again.  (2048 x 12288 x 4096, the
+// images and the product: 222 us and 233; with W as it is in binary16, right only at scales of
+// 2^-23 to 2^13, 226 and 230.)
+int form_of(int wf, int nmat, int dtype, int act) {
+    if (wf == WF_MXFP4) return dtype == DT_BF16 ? IMG_QUARTER : IMG_ROWS;
+    return sums_rest(wf, nmat, dtype, act) ? IMG_REST : IMG_F16;
+}
 Layout backward_layout(int nmat, int64_t M, int64_t N, int64_t K) {
     const int64_t slices = image_slices(N) * nmat;
-    return layout(plan_tiles(1, M, K, slices * 16), K / 32, slices, M, grad_sums_bytes(nmat, M, N));
+    return layout(plan_tiles(1, M, K, slices * 16), K / 32, slices, M, 0, grad_sums_bytes(nmat, M, N));
 }
 
 TileArgs tile_args(const Layout& l, uint8_t* ws) {
@@ -113,8 +124,9 @@ static int64_t few_part_row(int nmat, int64_t N) { return (N + 31) / 32 * nmat *
 // Whatever the activation.
 int64_t linear_workspace_bytes(int wf, int nmat, int dtype, int64_t M, int64_t N, int64_t K) {
     if (M > kFewCallMaxM) {
-        const int64_t one = forward_layout(nmat, false, M, N, K).total;
-        const int64_t two = wf != WF_MXFP4 && dtype == DT_F16 ? forward_layout(nmat, true, M, N, K).total : 0;
+        const bool mx = wf == WF_MXFP4;
+        const int64_t one = forward_layout(nmat, false, mx && dtype == DT_F16, M, N, K).total;
+        const int64_t two = !mx && dtype == DT_F16 ? forward_layout(nmat, true, false, M, N, K).total : 0;
         return one > two ? one : two;
     }
     const FewPlan p = plan_few(wf, nmat, few_rows_of(M), N, K);
@@ -173,15 +185,30 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
         t.epi = epilogue_args(a);
         return launch_tile_join(a.nmat, t, s);
     }
-    const bool rest = sums_rest(a.wf, a.nmat, a.dtype, a.act);
-    const Layout l = forward_layout(a.nmat, rest, a.M, a.N, a.K);
+    const int form = form_of(a.wf, a.nmat, a.dtype, a.act);
+    const Layout l = forward_layout(a.nmat, form == IMG_REST, form == IMG_ROWS, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, rest, ws, s);
-    if (e == hipSuccess)
-        e = launch_pack_x(a.x, a.dtype, a.M, a.K, rest, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at), s);
-    if (e != hipSuccess) return e;
     TileArgs t = tile_args(l, ws);
     t.epi = epilogue_args(a);
+    RowScaleArgs scales{};
+    if (form == IMG_ROWS) {
+        scales.mats = a.nmat;
+        scales.N = a.N;
+        scales.nb = a.K / 32;
+        scales.out = ws + l.scale_at;
+        for (int i = 0; i < a.nmat; i++) {
+            scales.s[i] = reinterpret_cast<const uint8_t*>(a.w[i].s);
+            t.epi.w_scale[i] = scales.out + i * (l.w_panels / a.nmat * 32);
+        }
+    }
+    if (form == IMG_QUARTER) {
+        t.bf16 = true;
+        t.xexp = nullptr;
+        t.unit = 4.0f;
+    }
+    hipError_t e = launch_pack_x(a.x, a.dtype, a.M, a.K, form == IMG_REST, ws + l.x_at, const_cast<int8_t*>(t.xexp), scales, s);
+    if (e == hipSuccess) e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, form, scales.out, ws, s);
+    if (e != hipSuccess) return e;
     return launch_tile_gemm(l.plan, a.nmat, t, s);
 }
 
@@ -192,7 +219,7 @@ int64_t linear_grad_workspace_bytes(int, int nmat, int64_t M, int64_t N, int64_t
 hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStream_t s) {
     const Layout l = backward_layout(a.nmat, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, false, ws, s);
+    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, IMG_F16, nullptr, ws, s);
     if (e == hipSuccess)
         e = launch_pack_dz(a, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at),
                            reinterpret_cast<float*>(ws + l.sums_at), s);

@@ -86,6 +86,18 @@ __device__ __forceinline__ u32x2_t mx_codes8(const float (&v)[8], uint32_t scale
     return r;
 }
 
+// The eight codes of a word times a quarter of their scale in bfloat16, exact under any:
+// 2^-130, the least, is a subnormal number of it, and 6 * 2^125 the largest.
+__device__ __forceinline__ u32x4_t bf16_quarters(uint32_t w, float s) {
+    const float f = 0.25f * s;
+    auto pair = [&](f32x2_t v) __attribute__((always_inline)) {
+        const f32x2_t t = {v[0] * f, v[1] * f};
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(t, bf16x2_t));
+    };
+    return u32x4_t{pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)), pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)),
+                   pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)), pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3))};
+}
+
 // Maximum over the four lanes of an aligned quad.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     uint32_t t = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);

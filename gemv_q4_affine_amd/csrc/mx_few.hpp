@@ -30,18 +30,6 @@ __device__ __forceinline__ uint32_t bf16_pair(uint32_t w, float s) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, B));
 }
 
-// The eight codes of a word times a quarter of their scale in bfloat16, exact under any:
-// 2^-130, the least, is a subnormal number of it, and 6 * 2^125 the largest.
-__device__ __forceinline__ u32x4_t bf16_quarters(uint32_t w, float s) {
-    const float f = 0.25f * s;
-    auto pair = [&](f32x2_t v) __attribute__((always_inline)) {
-        const f32x2_t t = {v[0] * f, v[1] * f};
-        return __builtin_bit_cast(uint32_t, __builtin_convertvector(t, bf16x2_t));
-    };
-    return u32x4_t{pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)), pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)),
-                   pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)), pair(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3))};
-}
-
 // 16-bit values with zeros in the place of infinities and NaN.
 template <int DT>
 __device__ __forceinline__ u32x4_t finite16(const u32x4_t& v) {

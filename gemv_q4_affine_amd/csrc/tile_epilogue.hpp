@@ -24,6 +24,14 @@ __device__ __forceinline__ void tile_epilogue(const floatx16_t (&acc)[NT][MT], f
     const int lane = threadIdx.x & 63;
     const int64_t N = epi.N, M = epi.M;
     const bool vec = N % 8 == 0;
+    // a lane's columns are the same in every turn (kChunks divides 64): their scales are read once
+    u32x2_t scale[2] = {};
+    if (EPI != EPI_PARTIAL && epi.w_scale[0]) {
+        const int64_t n = n0 + lane % kChunks * 8;
+#pragma unroll
+        for (int t = 0; t < (EPI == EPI_GATED ? 2 : 1); t++)
+            if (n < N) scale[t] = *reinterpret_cast<const u32x2_t*>(epi.w_scale[t] + n);
+    }
 #pragma unroll
     for (int j = 0; j < MT; j++) {
         const int64_t m0 = first + j * 32;
@@ -69,6 +77,10 @@ __device__ __forceinline__ void tile_epilogue(const floatx16_t (&acc)[NT][MT], f
                 }
             } else {
                 if (n >= N) continue;
+                if (epi.w_scale[0]) {
+                    unscale8(scale[0], z);
+                    if constexpr (EPI == EPI_GATED) unscale8(scale[1], z2);
+                }
                 if (vec) epilogue8<EPI, true>(epi, m, n, z, z2);
                 else epilogue8<EPI, false>(epi, m, n, z, z2);
             }

@@ -32,8 +32,10 @@
 namespace q4 {
 
 constexpr int kRing = 4;
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-template <int NT, int MT, int EPI>
+// BF: images in bfloat16, else in binary16.
+template <int NT, int MT, int EPI, bool BF>
 __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     static_assert(EPI != EPI_GATED || NT % 2 == 0, "gate and up panels come in pairs");
     constexpr int kPanels = 2 * (NT + MT);                  // of a slot: weights first
@@ -105,8 +107,12 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     };
     auto mfma = [&](int q, const u32x4_t (&fr)[NT + MT]) __attribute__((always_inline)) {
         const int i = q / MT, j = q % MT;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, fr[i]),
-                                                           __builtin_bit_cast(half8_t, fr[NT + j]), acc[i][j], 0, 0, 0);
+        if constexpr (BF)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fr[i]),
+                                                                __builtin_bit_cast(bf16x8_t, fr[NT + j]), acc[i][j], 0, 0, 0);
+        else
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, fr[i]),
+                                                               __builtin_bit_cast(half8_t, fr[NT + j]), acc[i][j], 0, 0, 0);
     };
 
     // ---- the schedule of a step: T MFMAs, the reads and copies between them ----
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     step_barrier<0>();
     tile_epilogue<NT, MT, EPI>(acc, reinterpret_cast<float*>(lds) + wave * 32 * kRowF, a.epi, a.part, part, a.w_panels,
                                EPI == EPI_GATED ? (pn0 + wn * NT) * 16 : (pn0 + wn * NT) * 32, (pm0 + wm * MT) * 32,
-                               [&](int64_t m) __attribute__((always_inline)) { return ldexpf(1.0f, -(int)a.xexp[m]); });
+                               [&](int64_t m) __attribute__((always_inline)) { return BF ? a.unit : ldexpf(1.0f, -(int)a.xexp[m]); });
 }
 
 // Sixteen columns of the sums of row groups by 256 threads, in k_join_sums's order:
@@ -229,6 +235,10 @@ __global__ __launch_bounds__(256) void k_tile_join(const TileArgs a, const unsig
         z[e] *= back;
         z2[e] *= back;
     }
+    if (a.epi.w_scale[0]) {
+        unscale8(*reinterpret_cast<const u32x2_t*>(a.epi.w_scale[0] + n), z);
+        if constexpr (EPI == EPI_GATED) unscale8(*reinterpret_cast<const u32x2_t*>(a.epi.w_scale[1] + n), z2);
+    }
     if (a.epi.N % 8 == 0) epilogue8<EPI, true>(a.epi, m, n, z, z2);
     else epilogue8<EPI, false>(a.epi, m, n, z, z2);
 }
@@ -270,11 +280,15 @@ int64_t partial_bytes(const TilePlan& p, int64_t M, int64_t w_panels) {
     return p.parts > 1 ? (int64_t)p.parts * M * w_panels * 32 * 4 : 0;
 }
 
+template <int NT, int MT, int EPI>
+static void launch_epi(const TileArgs& a, unsigned grid, hipStream_t s) {
+    hipLaunchKernelGGL((a.bf16 ? k_tile_gemm<NT, MT, EPI, true> : k_tile_gemm<NT, MT, EPI, false>), dim3(grid), dim3(256), 0, s, a);
+}
 template <int NT, int MT>
 static void launch_shape(int epi, const TileArgs& a, unsigned grid, hipStream_t s) {
-    if (epi == EPI_PARTIAL) hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_PARTIAL>), dim3(grid), dim3(256), 0, s, a);
-    else if (epi == EPI_GATED) hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_GATED>), dim3(grid), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_tile_gemm<NT, MT, EPI_LINEAR>), dim3(grid), dim3(256), 0, s, a);
+    if (epi == EPI_PARTIAL) launch_epi<NT, MT, EPI_PARTIAL>(a, grid, s);
+    else if (epi == EPI_GATED) launch_epi<NT, MT, EPI_GATED>(a, grid, s);
+    else launch_epi<NT, MT, EPI_LINEAR>(a, grid, s);
 }
 
 hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s) {

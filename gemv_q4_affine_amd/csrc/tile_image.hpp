@@ -1,8 +1,8 @@
-// tile_image.hpp -- the binary16 operand images of the dense matrix-core
+// tile_image.hpp -- the 16-bit operand images of the dense matrix-core
 // product (tile_gemm.hip) and the packers' device helpers (tile_pack.hip).
 //
-// An image holds the rows of an operand (weights or activations) in the order
-// in which v_mfma_f32_32x32x16_f16 reads them.  Rows go in panels of 32, the
+// An image holds the rows of an operand (weights or activations), in binary16 or
+// bfloat16, in the order in which v_mfma_f32_32x32x16_f16 (_bf16) reads them.  Rows go in panels of 32, the
 // summed index k in slices of 16; the unit of panel p and slice s is 1 KiB:
 // lane l's 16 bytes are row 32 p + (l & 31), k = 16 s + 8 (l >> 5) .. + 7.
 // Units of a panel are contiguous (slices first), so
@@ -41,7 +41,11 @@ struct EpilogueArgs {
     const void* residual;
     void* y;
     void* pre[2];
+    // Scale bytes of the weights' rows (padded to whole panels): the image holds a row under 2^13
+    // in the place of 2^(byte - 127).  Null: as they are.
+    const uint8_t* w_scale[2];
 };
+constexpr int kRowScale = 127 + 13;
 
 // The bias gradients: sums over groups of rows, [groups][nmat][N], joined in order
 // into the columns of out (null: none).
@@ -57,6 +61,7 @@ struct TileArgs {
     const uint8_t* wimg;
     const uint8_t* ximg;
     const int8_t* xexp;        // row m of the x image holds x * 2^xexp[m] (null: see unit)
+    bool bf16;                 // images in bfloat16 (no xexp), else in binary16
     int64_t slices;            // of both images
     int64_t w_panels, x_panels;
     int parts;                 // parts of the slices (EPI_PARTIAL), else 1
@@ -79,12 +84,25 @@ hipError_t launch_tile_gemm(const TilePlan& p, int nmat, const TileArgs& a, hipS
 hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s);
 // The weights as rows n (image of W) or as rows k (image of W^T, summed over
 // n); `mats` matrices side by side: panels alternate (rows n) or slices follow
-// each other (rows k).  `rest` (rows n): after K terms the roundings' remainders;
-// the activations' image then holds its rows twice.
-hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, bool rest,
-                               uint8_t* img, hipStream_t s);
+// each other (rows k).
+enum : int {
+    IMG_F16 = 0,       // in binary16
+    IMG_REST = 1,      // rows n: after K terms the roundings' remainders; the activations' image then holds its rows twice
+    IMG_ROWS = 2,      // MXFP4, rows n: under the scales of its rows (launch_pack_x's)
+    IMG_QUARTER = 3    // MXFP4, rows n: quarters in bfloat16
+};
+hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, int form,
+                               const uint8_t* row_scale, uint8_t* img, hipStream_t s);
+// The largest scale byte of every row of MXFP4 weights: out[mat * panels * 32 + n].
+struct RowScaleArgs {
+    const uint8_t* s[2];
+    int mats;                  // 0: none
+    int64_t N, nb;             // rows, scales of a row
+    uint8_t* out;
+};
+// dtype DT_BF16 and no xexp: the rows as they are, in bfloat16.
 hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool twice, uint8_t* img, int8_t* xexp,
-                         hipStream_t s);
+                         const RowScaleArgs& scales, hipStream_t s);
 // dz of every projection: the image, the dz outputs and the column sums.
 int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N);
 hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s);
@@ -148,6 +166,12 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int left, const u32x4
 #pragma unroll
     for (int e = 0; e < 8; e++)
         if (e < left) q[e] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
+}
+
+// Eight sums under the scale bytes of their columns' weights.
+__device__ __forceinline__ void unscale8(const u32x2_t& bytes, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = ldexpf(v[e], (int)((bytes[e >> 2] >> (8 * (e & 3))) & 0xFFu) - kRowScale);
 }
 
 // The epilogue of eight consecutive columns n .. n + 7 of row m (`left` of

@@ -1,6 +1,7 @@
 // tile_pack.hip -- the packers of the dense product's operand images
 // (tile_image.hpp): weights dequantised to binary16, by rows or transposed;
-// activations and gradients scaled to binary16 row by row.  All are bound by
+// activations and gradients scaled to binary16 row by row.  MXFP4 weights against
+// bfloat16 activations are images in bfloat16, the activations as they are.  All are bound by
 // memory (a quantised matrix read, two bytes a weight written).
 #include "mx_common.hpp"
 #include "tile_image.hpp"
@@ -10,8 +11,11 @@ namespace q4 {
 // ---- weights ---------------------------------------------------------------------
 //
 // Dequantised exactly in binary32 ((q - 8) d has 15 bits, q s + b one rounding)
-// and rounded once to binary16; MXFP4 codes are converted straight to binary16,
-// which holds them exactly at scales of 2^-23 to 2^13.
+// and rounded once to binary16.  MXFP4, whose scales may be any power of two:
+//   IMG_QUARTER  a quarter of each, which bfloat16 holds exactly under any scale;
+//   IMG_ROWS     binary16, a row's scales multiplied by the power of two that brings its
+//                largest to 2^13: exact from 2^-36 of that on;
+//   IMG_F16      (W^T) as they are: exact at scales of 2^-23 to 2^13.
 
 // Codes as binary32: byte e of w (8-bit), or its low / high nibble.
 template <int E>
@@ -49,12 +53,13 @@ __device__ __forceinline__ RowScale<WF> row_scale(const QuantW& w, int64_t n, in
 // the pieces of 16 bytes placed by an XOR with the row; then lane (row j, half h)
 // takes whole blocks of 32 weights, block 2 t + h in pass t, and writes each as
 // its four 16-byte pieces: for one piece 32 lanes write 512 contiguous bytes.
-// REST: the image has twice the slices, and the second half holds what the
+// IMG_REST: the image has twice the slices, and the second half holds what the
 // rounding to binary16 left of each weight (see launch_linear).
 // Measured: two 12288 x 4096 Q4_0 matrices 44 us, 57 MB read and 201 MB written.
-template <int WF, bool REST>
+template <int WF, int FORM>
 __global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int mats, int N, int64_t K, int64_t slices,
-                                                      int64_t kgroups, uint8_t* __restrict__ img) {
+                                                      int64_t kgroups, const uint8_t* __restrict__ row_scales,
+                                                      uint8_t* __restrict__ img) {
     constexpr int kBlocks = WF == WF_AFFINE8 ? 4 : 8;        // of 32 weights, in a wave's 128 bytes of a row
     constexpr int kPieces = 8 / kBlocks;                     // 16-byte pieces of a block
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * 32 * 128];
@@ -77,11 +82,18 @@ __global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int 
     }
     const int64_t n = first + (j < in ? j : in);
     RowScale<WF> sc[kBlocks / 2];
+    int largest = 0;
+    if constexpr (FORM == IMG_ROWS) largest = row_scales[(mats == 2 && (panel & 1) ? ((int64_t)N + 31) / 32 * 32 : 0) + n];
 #pragma unroll
     for (int t = 0; t < kBlocks / 2; t++) {
         int64_t b = b0 + 2 * t + h;
         b = b < nb ? b : nb - 1;
-        sc[t] = row_scale<WF>(w, n, b, K);
+        if constexpr (FORM == IMG_ROWS) {
+            const int s = reinterpret_cast<const uint8_t*>(w.s)[n * nb + b], to = s - largest + kRowScale;
+            sc[t] = {mx_scale(s == 255 ? 255u : to < 1 ? 1u : (uint32_t)to), 0.0f};
+        } else {
+            sc[t] = row_scale<WF>(w, n, b, K);
+        }
     }
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     Q4_WAIT_VMCNT(0);
@@ -98,7 +110,8 @@ __global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int 
 #pragma unroll
         for (int c = 0; c < 4; c++) {        // elements 8 c .. 8 c + 7: slice c / 2, half c % 2
             if constexpr (WF == WF_MXFP4) {
-                *reinterpret_cast<u32x4_t*>(out + (c >> 1) * kUnit + (c & 1) * 512) = mx_pairs(raw[0][c], sc[t].s);
+                *reinterpret_cast<u32x4_t*>(out + (c >> 1) * kUnit + (c & 1) * 512) =
+                    FORM == IMG_QUARTER ? bf16_quarters(raw[0][c], sc[t].s) : mx_pairs(raw[0][c], sc[t].s);
                 continue;
             }
             float f[8];
@@ -122,7 +135,7 @@ __global__ __launch_bounds__(256) void k_pack_weights(QuantW w0, QuantW w1, int 
             for (int e = 0; e < 8; e++) f[e] = sc[t](f[e]);
             const u32x4_t v = pack8(DT_F16, f);
             *reinterpret_cast<u32x4_t*>(out + (c >> 1) * kUnit + (c & 1) * 512) = v;
-            if constexpr (REST) {
+            if constexpr (FORM == IMG_REST) {
                 float rounded[8];
                 unpack8(DT_F16, v, rounded);
 #pragma unroll
@@ -223,16 +236,17 @@ __global__ __launch_bounds__(256) void k_pack_weights_t(QuantW w0, QuantW w1, in
 }
 
 template <int WF>
-static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, bool rest, uint8_t* img,
-                                 hipStream_t s) {
+static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, int form,
+                                 const uint8_t* row_scale, uint8_t* img, hipStream_t s) {
     if (!transposed) {
         constexpr int kGroupK = WF == WF_AFFINE8 ? 512 : 1024;
         const int64_t kgroups = (K + kGroupK - 1) / kGroupK, blocks = (N + 31) / 32 * mats * kgroups;
         if (!launchable(blocks, 256)) return hipErrorInvalidValue;
-        auto k = k_pack_weights<WF, false>;
-        if constexpr (WF != WF_MXFP4) k = rest ? k_pack_weights<WF, true> : k;
-        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), 0,
-                           s, w[0], w[mats - 1], mats, (int)N, K, image_slices(K) * (rest ? 2 : 1), kgroups, img);
+        constexpr bool kMx = WF == WF_MXFP4;
+        auto k = form == IMG_REST || form == IMG_ROWS ? k_pack_weights<WF, kMx ? IMG_ROWS : IMG_REST>
+                                                      : k_pack_weights<WF, kMx ? IMG_QUARTER : IMG_F16>;
+        hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), 0, s, w[0], w[mats - 1], mats, (int)N, K,
+                           image_slices(K) * (form == IMG_REST ? 2 : 1), kgroups, row_scale, img);
     } else {
         constexpr int kTileK = WF == WF_AFFINE8 ? 128 : 256;
         const int64_t ktiles = (K + kTileK - 1) / kTileK, ntiles = (N + 63) / 64, blocks = ktiles * ntiles * mats;
@@ -243,12 +257,12 @@ static hipError_t pack_weights_t(int mats, const QuantW* w, int64_t N, int64_t K
     return hipGetLastError();
 }
 
-hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, bool rest,
-                               uint8_t* img, hipStream_t s) {
-    if (wf == WF_Q4_0) return pack_weights_t<WF_Q4_0>(mats, w, N, K, transposed, rest, img, s);
-    if (wf == WF_AFFINE4) return pack_weights_t<WF_AFFINE4>(mats, w, N, K, transposed, rest, img, s);
-    if (wf == WF_MXFP4) return pack_weights_t<WF_MXFP4>(mats, w, N, K, transposed, rest, img, s);
-    return pack_weights_t<WF_AFFINE8>(mats, w, N, K, transposed, rest, img, s);
+hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, int form,
+                               const uint8_t* row_scale, uint8_t* img, hipStream_t s) {
+    if (wf == WF_Q4_0) return pack_weights_t<WF_Q4_0>(mats, w, N, K, transposed, form, row_scale, img, s);
+    if (wf == WF_AFFINE4) return pack_weights_t<WF_AFFINE4>(mats, w, N, K, transposed, form, row_scale, img, s);
+    if (wf == WF_MXFP4) return pack_weights_t<WF_MXFP4>(mats, w, N, K, transposed, form, row_scale, img, s);
+    return pack_weights_t<WF_AFFINE8>(mats, w, N, K, transposed, form, row_scale, img, s);
 }
 
 // ---- rows of activations and gradients ----------------------------------------------
@@ -296,21 +310,69 @@ __device__ __forceinline__ float max8(const float (&v)[8], float mx) {
     return mx;
 }
 
-template <int ROWS>
+// Before them the workgroups that find the scales of W's rows (RowScaleArgs): eight
+// lanes a row, 16 bytes each at a time.
+constexpr int kScaleRows = kPackThreads / 8;
+
+__device__ __forceinline__ void row_scales(const RowScaleArgs& a, int64_t block) {
+    typedef u32x4_t u32x4_b __attribute__((aligned(1)));
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    const int64_t np = (a.N + 31) / 32 * 32, id = block * kScaleRows + threadIdx.x / 8;
+    if (id >= np * a.mats) return;
+    const int64_t n = id % np, last = n < a.N ? n : a.N - 1;
+    const uint8_t* row = a.s[id / np] + last * a.nb;
+    // largest byte + 1, with 255 (a NaN) as 0: pairs of bytes as 16-bit numbers
+    u16x2_t most = {0, 0};
+    auto take = [&](uint32_t pair) __attribute__((always_inline)) {
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, (pair + 0x00010001u) & 0x00FF00FFu));
+    };
+    const int t = threadIdx.x & 7;
+    for (int64_t i = t * 16; i + 16 <= a.nb; i += 128) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_b*>(row + i);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            take(v[e] & 0x00FF00FFu);
+            take(v[e] >> 8 & 0x00FF00FFu);
+        }
+    }
+    for (int64_t i = a.nb / 16 * 16 + t; i < a.nb; i += 8) take(row[i]);
+    uint32_t m = most[0] > most[1] ? most[0] : most[1];
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
+        m = o > m ? o : m;
+    }
+    if (t == 0) a.out[id] = (uint8_t)(m > 0u ? m - 1u : 0u);
+}
+
+// AS_IS: bfloat16 rows, copied.
+template <int ROWS, bool AS_IS>
 __global__ __launch_bounds__(kPackThreads) void k_pack_rows(const void* __restrict__ x, int dtype, int64_t M, int64_t K,
                                                             int64_t slices, int twice, uint8_t* __restrict__ img,
-                                                            int8_t* __restrict__ xexp) {
+                                                            int8_t* __restrict__ xexp, const RowScaleArgs scales,
+                                                            const unsigned scale_blocks) {
+    if (blockIdx.x < scale_blocks) {
+        row_scales(scales, blockIdx.x);
+        return;
+    }
     __shared__ float red[kPackThreads / 64][8];
     const int lane = threadIdx.x & 63;
     constexpr int kStride = kPackThreads / ROWS;
-    const int64_t m = (int64_t)blockIdx.x * ROWS + lane % ROWS, c0 = (threadIdx.x >> 6) * (64 / ROWS) + lane / ROWS;
+    const int64_t m = (int64_t)(blockIdx.x - scale_blocks) * ROWS + lane % ROWS, c0 = (threadIdx.x >> 6) * (64 / ROWS) + lane / ROWS;
     const int64_t row = (m < M ? m : M - 1) * K, chunks = K / 8;          // K % 32 == 0
+    if constexpr (AS_IS) {
+        if (m < M)
+            for (int64_t c = c0; c < chunks; c += kStride)
+                *reinterpret_cast<u32x4_t*>(piece(img, m, slices, c)) = load8_raw<true>(x, row + c * 8, 8);
+        return;
+    }
     float v[8], mx = 0.0f;
     for (int64_t c = c0; c < chunks; c += kStride) {
         unpack8(dtype, load8_raw<true>(x, row + c * 8, 8), v);
         mx = max8(v, mx);
     }
-    const int e = row_exponent(rows_max<ROWS>(mx, red));
+    int e = row_exponent(rows_max<ROWS>(mx, red));
+    if (scales.mats > 0 && e < 0) e = 0;                     // binary16 rows against scaled weights: exact
     const float scale = ldexpf(1.0f, e);
     if (m < M) {
         for (int64_t c = c0; c < chunks; c += kStride) {
@@ -337,14 +399,20 @@ static int pack_rows(int64_t M) { return M > 8 * (current_cu_count() - 1) ? 8 : 
 constexpr int64_t kLaunchRows = int64_t(1) << 24;
 
 hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool twice, uint8_t* img, int8_t* xexp,
-                         hipStream_t s) {
+                         const RowScaleArgs& scales, hipStream_t s) {
     const int rows = pack_rows(M);
     const int64_t slices = image_slices(K) * (twice ? 2 : 1);
-    for (int64_t m = 0; m < M; m += kLaunchRows) {
+    const bool as_is = !xexp;
+    auto k = rows == 8 ? (as_is ? k_pack_rows<8, true> : k_pack_rows<8, false>)
+                       : (as_is ? k_pack_rows<4, true> : k_pack_rows<4, false>);
+    // (at most 2^26 rows of W: 2^19 workgroups)
+    unsigned scale_blocks = (unsigned)(((scales.N + 31) / 32 * 32 * scales.mats + kScaleRows - 1) / kScaleRows);
+    for (int64_t m = 0; m < M; m += kLaunchRows, scale_blocks = 0) {
         const int64_t count = M - m < kLaunchRows ? M - m : kLaunchRows;
-        hipLaunchKernelGGL(rows == 8 ? k_pack_rows<8> : k_pack_rows<4>, dim3((unsigned)((count + rows - 1) / rows)),
-                           dim3(kPackThreads), 0, s, static_cast<const char*>(x) + m * K * 2, dtype, count, K, slices,
-                           twice ? 1 : 0, img + m / 32 * slices * kUnit, xexp + m);
+        if (!launchable(scale_blocks + (count + rows - 1) / rows, kPackThreads)) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(k, dim3(scale_blocks + (unsigned)((count + rows - 1) / rows)), dim3(kPackThreads), 0, s,
+                           static_cast<const char*>(x) + m * K * 2, dtype, count, K, slices, twice ? 1 : 0,
+                           img + m / 32 * slices * kUnit, as_is ? nullptr : xexp + m, scales, scale_blocks);
     }
     return hipGetLastError();
 }

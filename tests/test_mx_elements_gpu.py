@@ -1,0 +1,205 @@
+"""The products on microscaled numbers element by element, on every route: each output within its own rounding and a
+bound of its own sum's error, so that no wrong element hides among many.
+
+The bounds, from the arithmetic.  With T = sum |x| |w| of an output's K terms:
+  * K binary32 roundings of partial sums, each at most T 2^-24, and a few of the epilogue's;
+  * MXFP8 x: a matrix instruction cuts a step's products 2^-16 below the largest of them.  A step lies inside 512
+    consecutive k, so the largest is at most that of |x| there times that of |w|; 2^-16 of it for each product;
+  * gradients: dz goes into the product in binary16, 2^-12 of each term (and 2^-39 of its row's largest dz).
+An activation's slope is at most 1.13; a second factor, itself off by its bound, multiplies the first one's."""
+import math
+
+import pytest
+import torch
+
+import gemv_q4_affine_amd as Q
+from test_mx_gpu import ACTS, say
+from test_mx_range_gpu import weights
+from test_mx_wide_gpu import planes, values
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(autouse=True)
+def _done():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    yield
+    torch.cuda.synchronize()
+
+
+def eps(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def within(got, want, bound, what):
+    """|got - want| <= the output's rounding + bound, everywhere; an output past its type's range is an infinity."""
+    top = torch.finfo(got.dtype).max
+    past = want.abs() - bound > top * (1 + eps(got.dtype))
+    inside = want.abs() + bound < top
+    slack = want.abs() * eps(got.dtype) + bound * (1 + eps(got.dtype)) + (2.0 ** -25 if got.dtype == torch.float16 else 0.0)
+    e = ((got.double() - want).abs() / slack)[inside]
+    say(f"  {what}: {e.max().item():.3g} of the slack, {(slack / want.abs()).median().item():.2g} of the median output")
+    assert torch.isfinite(got[inside]).all() and (e <= 1).all(), what
+    assert (got[past] == want[past].sign() * math.inf).all(), what
+
+
+def activation(x, M, K, seed):
+    """x as the calls take it, its binary64 values."""
+    if x in DT:
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        v = torch.randn(M, K, generator=gen, device="cuda").to(DT[x])
+        return v, v.double()
+    p = planes(M, K, 8 if x == "fp8" else 4, seed)
+    return p, values(p)
+
+
+def sums(x, X, W):
+    """The exact sums, the bound of the computed ones' errors."""
+    K = X.shape[1]
+    bound = (X.abs() @ W.abs().T) * ((K + 8) * 2.0 ** -24)
+    if x == "fp8":
+        pad = (512 - K % 512) % 512
+        most = [torch.nn.functional.pad(t.abs(), (0, pad)).view(t.shape[0], -1, 512).amax(2) for t in (X, W)]
+        bound += most[0] @ most[1].T * min(K, 512) * 2.0 ** -16
+    return X @ W.T, bound
+
+
+def act64(z, kind):
+    if kind == "silu":
+        return z * torch.sigmoid(z)
+    if kind == "gelu":
+        return z * 0.5 * torch.erfc(-z / math.sqrt(2))
+    if kind == "gelu_tanh":
+        return z * 0.5 * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
+    return z.clamp(min=0) if kind == "relu" else z
+
+
+def activated(z, bound, kind):
+    """act(z), the bound of its error: the slope's, and the kernels' exponentials' (2^-21 of |z|)."""
+    return act64(z, kind), bound * (1.0 if kind in ("none", "relu") else 1.13) + (0.0 if kind in ("none", "relu") else z.abs() * 2.0 ** -21)
+
+
+def check_linear(x, M, N, K, dt, act, full, seed=1):
+    say(f"linear x={x} {M} x {N} x {K} {act} {dt}")
+    w = planes(N, K, 4, seed)
+    xq, X64 = activation(x, M, K, seed + 1)
+    z, e = sums(x, X64, values(w))
+    b = r = None
+    if full:
+        gen = torch.Generator(device="cuda").manual_seed(seed + 2)
+        b, r = (torch.randn(*s, generator=gen, device="cuda").to(DT[dt]) for s in ((N,), (M, N)))
+        z = z + b.double()
+        e = e + z.abs() * 2.0 ** -23
+    got = Q.mx_linear(w, xq, bias=b, act=ACTS[act], residual=r, save_pre=full, dtype=DT[dt])
+    y, ey = activated(z, e, act)
+    if full:
+        within(got[1], z, e, "pre")
+        y = y + r.double()
+        ey = ey + y.abs() * 2.0 ** -23
+    within(got[0] if full else got, y, ey, "y")
+
+
+def check_gated(x, M, N, K, dt, act, save, seed=1):
+    say(f"gated x={x} {M} x {N} x {K} {act} {dt}")
+    g, u = planes(N, K, 4, seed), planes(N, K, 4, seed + 3)
+    xq, X64 = activation(x, M, K, seed + 1)
+    (zg, eg), (zu, eu) = sums(x, X64, values(g)), sums(x, X64, values(u))
+    got = Q.mx_gated(g, u, xq, act=ACTS[act], save_pre=save, dtype=DT[dt])
+    a, ea = activated(zg, eg, act)
+    if save:
+        within(got[1], zg, eg, "gate")
+        within(got[2], zu, eu, "up")
+    within(got[0] if save else got, a * zu, ea * zu.abs() + a.abs() * eu + ea * eu + (a * zu).abs() * 2.0 ** -23, "h")
+
+
+# ---- images: 16-bit x at many rows ------------------------------------------------------
+
+#: Ragged columns, split sums, one and several tiles, rows that end inside a tile.
+IMAGES = {"bf16": [(700, 8201, 544), (300, 1000, 16384), (260, 1001, 16384), (1000, 2053, 2080), (129, 20001, 1056)],
+          "f16": [(65, 130, 96), (100, 1001, 16384), (300, 523, 704), (700, 8201, 544), (65, 33, 8192)]}
+
+
+def image_bytes(M, N, K, nmat):
+    return ((N + 31) // 32 * nmat + (M + 31) // 32) * 32 * K * 2
+
+
+@pytest.mark.parametrize("x,M,N,K", [(x, *s) for x in IMAGES for s in IMAGES[x]])
+def test_images(x, M, N, K):
+    kind = {"bf16": Q.binding.Q4_BF16, "f16": Q.binding.Q4_F16}[x]
+    assert Q.mx_linear_workspace_size(M, N, K, kind) >= image_bytes(M, N, K, 1)        # the route that is meant
+    assert Q.mx_gated_workspace_size(M, N, K, kind) >= image_bytes(M, N, K, 2)
+    check_linear(x, M, N, K, x, "none", False)
+    check_linear(x, M, N, K, x, "gelu", True)
+    check_gated(x, M, N, K, x, "silu", True)
+    check_gated(x, M, N, K, x, "relu", False)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_split_sums_are_among_them(x):
+    kind = {"bf16": Q.binding.Q4_BF16, "f16": Q.binding.Q4_F16}[x]
+    assert any(Q.mx_linear_workspace_size(*s, kind) >= image_bytes(*s, 1) + 8 * s[0] * s[1] for s in IMAGES[x])
+
+
+@pytest.mark.parametrize("x,M,N,K", [("bf16", 700, 8201, 544), ("bf16", 260, 1001, 16384), ("f16", 70, 1001, 544), ("f16", 100, 300, 16384)])
+def test_images_of_spoilt_rows_and_columns(x, M, N, K):
+    assert Q.mx_linear_workspace_size(M, N, K, {"bf16": Q.binding.Q4_BF16, "f16": Q.binding.Q4_F16}[x]) >= image_bytes(M, N, K, 1)
+    w = planes(N, K, 4, 1)
+    v, _ = activation(x, M, K, 2)
+    clean = Q.mx_linear(w, v)
+    row, cols = M // 2, [7, N - 1]
+    bad_w = (w[0], w[1].clone())
+    bad_w[1][7, 3] = bad_w[1][N - 1, K // 32 - 1] = 255
+    bad = v.clone()
+    bad[row, 17] = math.nan
+    want = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    want[row], want[:, cols] = True, True
+    y = Q.mx_linear(bad_w, bad)
+    assert torch.equal(torch.isnan(y), want) and torch.equal(y[~want], clean[~want])
+    h = Q.mx_gated(w, bad_w, bad)
+    assert torch.equal(torch.isnan(h), want)
+    bad = v.clone()
+    bad[row, 5] = math.inf
+    got, col = Q.mx_linear(w, bad), values(w)[:, 5]
+    others = torch.arange(M, device="cuda") != row
+    assert torch.equal(got[others], clean[others])
+    assert torch.equal(torch.isnan(got[row]), col == 0)
+    assert (got[row][col > 0] == math.inf).all() and (got[row][col < 0] == -math.inf).all()
+
+
+@pytest.mark.parametrize("x,M,N,K", [("bf16", 260, 1001, 16384), ("bf16", 700, 8201, 544), ("f16", 100, 300, 16384), ("f16", 70, 130, 96)])
+def test_images_captured(x, M, N, K):
+    assert Q.mx_linear_workspace_size(M, N, K, {"bf16": Q.binding.Q4_BF16, "f16": Q.binding.Q4_F16}[x]) > 0
+    w, u = planes(N, K, 4, 1), planes(N, K, 4, 2)
+    xs = [activation(x, M, K, s)[0] for s in (3, 4, 5)]
+    f = lambda v: (Q.mx_linear(w, v, act=ACTS["silu"]), Q.mx_gated(w, u, v))  # noqa: E731
+    want = [f(v) for v in xs]
+    live = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f(live)
+    for k in (1, 2, 0, 1):
+        live.copy_(xs[k])
+        graph.replay()
+        f(xs[(k + 1) % 3])                                   # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[k])), k
+
+
+def test_images_of_rows_of_one_scale():
+    """binary16 x: rows of W under scales from the first to the last, a NaN among them, and rows of NaN scales only."""
+    M, K = 80, 352
+    s = torch.randint(100, 150, (300, K // 32), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    w, W = weights(s, 2)
+    bad = (w[0], w[1].clone())
+    bad[1][4], bad[1][9, 2], bad[1][12, 10] = 255, 255, 255
+    v, v64 = activation("f16", M, K, 3)
+    y, z = Q.mx_linear(w, v), Q.mx_linear(bad, v)
+    want, e = sums("f16", v64, W)
+    within(y, want, e, "y")
+    spoilt = torch.tensor([4, 9, 12], device="cuda")
+    assert torch.isnan(z[:, spoilt]).all()
+    fine = torch.ones(300, dtype=torch.bool, device="cuda")
+    fine[spoilt] = False
+    assert torch.equal(z[:, fine], y[:, fine])

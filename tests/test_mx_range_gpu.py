@@ -114,7 +114,8 @@ def by_element(got, x, W, what, extra=0.0):
 
 
 #: 255 rows of W, each under a scale of its own, times `more`; the routes by rows, on 16-bit x.
-ROUTES = [(1, 1, 160), (4, 1, 2080), (5, 1, 160), (20, 1, 544), (40, 1, 8192), (64, 1, 160)]
+ROUTES = [(1, 1, 160), (4, 1, 2080), (5, 1, 160), (20, 1, 544), (40, 1, 8192), (64, 1, 160), (65, 1, 160), (100, 1, 544), (300, 1, 544),
+          (700, 32, 544)]
 
 
 @pytest.mark.parametrize("x", ["bf16", "f16"])
