@@ -19,9 +19,9 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 // exponents, parts of a split sum, column sums.
 struct Layout {
     TilePlan plan;
-    int64_t slices, w_panels, x_panels, x_at, exp_at, scale_at, part_at, sums_at, total;
+    int64_t slices, w_panels, x_panels, x_at, exp_at, scale_at, most_at, part_at, sums_at, total;
 };
-Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M, int64_t scales, int64_t sums) {
+Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M, int64_t scales, int64_t most, int64_t sums) {
     Layout l{};
     l.plan = plan;
     l.slices = slices;
@@ -30,7 +30,8 @@ Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M,
     l.x_at = up256(w_panels * slices * kUnit);
     l.exp_at = l.x_at + l.x_panels * slices * kUnit;
     l.scale_at = l.exp_at + up256(M);
-    l.part_at = l.scale_at + up256(scales);
+    l.most_at = l.scale_at + up256(scales);
+    l.part_at = l.most_at + up256(most);
     l.sums_at = l.part_at + partial_bytes(plan, M, w_panels);
     l.total = l.sums_at + sums;
     return l;
@@ -40,7 +41,7 @@ Layout layout(const TilePlan& plan, int64_t w_panels, int64_t slices, int64_t M,
 Layout forward_layout(int nmat, bool rest, bool row_scales, int64_t M, int64_t N, int64_t K) {
     if (rest) K *= 2;
     const int64_t w_panels = (N + 31) / 32 * nmat;
-    return layout(plan_tiles(nmat, M, N, K), w_panels, image_slices(K), M, row_scales ? w_panels * 32 : 0, 0);
+    return layout(plan_tiles(nmat, M, N, K), w_panels, image_slices(K), M, row_scales ? w_panels * 32 : 0, 0, 0);
 }
 // A weight rounded to binary16 puts about as much error into a sum as the
 // rounding of a binary16 output does.  One such error (q4_linear with no
@@ -61,9 +62,11 @@ int form_of(int wf, int nmat, int dtype, int act) {
     if (wf == WF_MXFP4) return dtype == DT_BF16 ? IMG_QUARTER : IMG_ROWS;
     return sums_rest(wf, nmat, dtype, act) ? IMG_REST : IMG_F16;
 }
-Layout backward_layout(int nmat, int64_t M, int64_t N, int64_t K) {
+Layout backward_layout(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
     const int64_t slices = image_slices(N) * nmat;
-    return layout(plan_tiles(1, M, K, slices * 16), K / 32, slices, M, 0, grad_sums_bytes(nmat, M, N));
+    const bool mx = wf == WF_MXFP4;
+    return layout(plan_tiles(1, M, K, slices * 16), K / 32, slices, M, mx ? K : 0, mx ? K / 32 * kScaleParts : 0,
+                  grad_sums_bytes(nmat, M, N));
 }
 
 TileArgs tile_args(const Layout& l, uint8_t* ws) {
@@ -75,6 +78,17 @@ TileArgs tile_args(const Layout& l, uint8_t* ws) {
     t.w_panels = l.w_panels;
     t.x_panels = l.x_panels;
     t.part = reinterpret_cast<float*>(ws + l.part_at);
+    return t;
+}
+template <class Args>
+ScaleArgs scale_args(const Args& a, const Layout& l, uint8_t* ws) {
+    ScaleArgs t{};
+    for (int i = 0; i < a.nmat; i++) t.s[i] = reinterpret_cast<const uint8_t*>(a.w[i].s);
+    t.mats = a.nmat;
+    t.N = a.N;
+    t.nb = a.K / 32;
+    t.out = ws + l.scale_at;
+    t.part = ws + l.most_at;
     return t;
 }
 
@@ -190,39 +204,33 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     TileArgs t = tile_args(l, ws);
     t.epi = epilogue_args(a);
-    RowScaleArgs scales{};
-    if (form == IMG_ROWS) {
-        scales.mats = a.nmat;
-        scales.N = a.N;
-        scales.nb = a.K / 32;
-        scales.out = ws + l.scale_at;
-        for (int i = 0; i < a.nmat; i++) {
-            scales.s[i] = reinterpret_cast<const uint8_t*>(a.w[i].s);
-            t.epi.w_scale[i] = scales.out + i * (l.w_panels / a.nmat * 32);
-        }
-    }
+    const ScaleArgs scales = form == IMG_ROWS ? scale_args(a, l, ws) : ScaleArgs{};
+    if (form == IMG_ROWS)
+        for (int i = 0; i < a.nmat; i++) t.epi.w_scale[i] = scales.out + i * (l.w_panels / a.nmat * 32);
     if (form == IMG_QUARTER) {
         t.bf16 = true;
         t.xexp = nullptr;
         t.unit = 4.0f;
     }
     hipError_t e = launch_pack_x(a.x, a.dtype, a.M, a.K, form == IMG_REST, ws + l.x_at, const_cast<int8_t*>(t.xexp), scales, s);
-    if (e == hipSuccess) e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, form, scales.out, ws, s);
+    if (e == hipSuccess) e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, form, scales, ws, s);
     if (e != hipSuccess) return e;
     return launch_tile_gemm(l.plan, a.nmat, t, s);
 }
 
-int64_t linear_grad_workspace_bytes(int, int nmat, int64_t M, int64_t N, int64_t K) {
-    return backward_layout(nmat, M, N, K).total;
+int64_t linear_grad_workspace_bytes(int wf, int nmat, int64_t M, int64_t N, int64_t K) {
+    return backward_layout(wf, nmat, M, N, K).total;
 }
 
 hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStream_t s) {
-    const Layout l = backward_layout(a.nmat, a.M, a.N, a.K);
+    const Layout l = backward_layout(a.wf, a.nmat, a.M, a.N, a.K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    hipError_t e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, IMG_F16, nullptr, ws, s);
-    if (e == hipSuccess)
-        e = launch_pack_dz(a, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at),
-                           reinterpret_cast<float*>(ws + l.sums_at), s);
+    const bool mx = a.wf == WF_MXFP4;
+    ScaleArgs scales = mx ? scale_args(a, l, ws) : ScaleArgs{};
+    scales.parts = scale_parts(a.M, a.K / 32);
+    hipError_t e = launch_pack_dz(a, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at),
+                                  reinterpret_cast<float*>(ws + l.sums_at), scales, s);
+    if (e == hipSuccess) e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, mx ? IMG_ROWS : IMG_F16, scales, ws, s);
     if (e != hipSuccess) return e;
     // the bias gradients' join goes with the parts' where the product is split
     // (MXFP4, 1001 x 8192 x 2048: 71.0 us against 73.4 with a launch of its own, 200 x 1024 x 1024 23.0 and 25.9)
@@ -230,6 +238,7 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStrea
     TileArgs t = tile_args(l, ws);
     if (l.plan.parts > 1) t.sums = sums;
     else if ((e = launch_join_sums(sums, s)) != hipSuccess) return e;
+    t.epi.w_scale[0] = scales.out;
     t.epi.act = ACT_NONE;
     t.epi.dtype = DT_BF16;
     t.epi.M = a.M;

@@ -12,7 +12,7 @@ template <int NT>
 constexpr int tile_row_floats() { return NT * 32 + 4; }
 
 // The wave's NT x MT accumulator tiles of 32 x 32 (columns n0 .., at EPI_GATED
-// panels of gate and up in turn; rows first ..), scaled by back(m) -- not the parts
+// panels of gate and up in turn; rows first ..), times 2^back(m) -- not the parts
 // of a split sum, which are joined first: alone they may leave the range.
 template <int NT, int MT, int EPI, class Back>
 __device__ __forceinline__ void tile_epilogue(const floatx16_t (&acc)[NT][MT], float* tile, const EpilogueArgs& epi,
@@ -24,19 +24,30 @@ __device__ __forceinline__ void tile_epilogue(const floatx16_t (&acc)[NT][MT], f
     const int lane = threadIdx.x & 63;
     const int64_t N = epi.N, M = epi.M;
     const bool vec = N % 8 == 0;
-    // a lane's columns are the same in every turn (kChunks divides 64): their scales are read once
-    u32x2_t scale[2] = {};
-    if (EPI != EPI_PARTIAL && epi.w_scale[0]) {
-        const int64_t n = n0 + lane % kChunks * 8;
+    // Columns with powers of two of their own: a lane's are the same in every turn (kChunks
+    // divides 64) and found once.
+    const bool scaled = EPI != EPI_PARTIAL && epi.w_scale[0];
+    constexpr int kFactors = EPI == EPI_GATED ? 2 : 1;
+    u32x2_t scale[kFactors] = {};
+    float factor[kFactors][8];
 #pragma unroll
-        for (int t = 0; t < (EPI == EPI_GATED ? 2 : 1); t++)
-            if (n < N) scale[t] = *reinterpret_cast<const u32x2_t*>(epi.w_scale[t] + n);
+    for (int t = 0; t < kFactors; t++) {
+        const int64_t n = n0 + lane % kChunks * 8;
+        if (scaled && n < N) scale[t] = *reinterpret_cast<const u32x2_t*>(epi.w_scale[t] + n);
+#pragma unroll
+        for (int e = 0; e < 8; e++) factor[t][e] = 1.0f;
+        unscale8(scale[t], 0, factor[t]);
     }
 #pragma unroll
     for (int j = 0; j < MT; j++) {
         const int64_t m0 = first + j * 32;
         const int64_t mine = m0 + (lane & 31);
-        const float back = EPI == EPI_PARTIAL ? 1.0f : mine < M ? back_of(mine) : 0.0f;
+        const int by = EPI != EPI_PARTIAL && mine < M ? back_of(mine) : 0;
+        // (sums lie between 2^-48 and 2^57: beyond 2^+-64 a row's power of two and a column's go
+        // together, as halfway the value may leave the range; the row's waits behind the row)
+        const bool far = scaled && __any(by < -64 || by > 64);
+        const float back = far ? 1.0f : ldexpf(1.0f, by);
+        if (far) tile[(lane & 31) * kRowF + NT * 32] = __int_as_float(by);
         // lane: row lane & 31 of the panel, columns 8 (e / 4) + 4 (lane >> 5) + e % 4
 #pragma unroll
         for (int i = 0; i < NT; i++)
@@ -77,9 +88,16 @@ __device__ __forceinline__ void tile_epilogue(const floatx16_t (&acc)[NT][MT], f
                 }
             } else {
                 if (n >= N) continue;
-                if (epi.w_scale[0]) {
-                    unscale8(scale[0], z);
-                    if constexpr (EPI == EPI_GATED) unscale8(scale[1], z2);
+                if (far) {
+                    const int e = __float_as_int(tile[row * kRowF + NT * 32]);
+                    unscale8(scale[0], e, z);
+                    if constexpr (EPI == EPI_GATED) unscale8(scale[1], e, z2);
+                } else if (scaled) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        z[e] *= factor[0][e];
+                        if constexpr (EPI == EPI_GATED) z2[e] *= factor[1][e];
+                    }
                 }
                 if (vec) epilogue8<EPI, true>(epi, m, n, z, z2);
                 else epilogue8<EPI, false>(epi, m, n, z, z2);

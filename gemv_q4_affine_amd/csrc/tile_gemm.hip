@@ -176,7 +176,7 @@ __global__ __launch_bounds__(256, 1) void k_tile_gemm(const TileArgs a) {
     step_barrier<0>();
     tile_epilogue<NT, MT, EPI>(acc, reinterpret_cast<float*>(lds) + wave * 32 * kRowF, a.epi, a.part, part, a.w_panels,
                                EPI == EPI_GATED ? (pn0 + wn * NT) * 16 : (pn0 + wn * NT) * 32, (pm0 + wm * MT) * 32,
-                               [&](int64_t m) __attribute__((always_inline)) { return BF ? a.unit : ldexpf(1.0f, -(int)a.xexp[m]); });
+                               [&](int64_t m) __attribute__((always_inline)) { return BF ? 2 : -(int)a.xexp[m]; });      // (quarters)
 }
 
 // Sixteen columns of the sums of row groups by 256 threads, in k_join_sums's order:
@@ -229,15 +229,17 @@ __global__ __launch_bounds__(256) void k_tile_join(const TileArgs a, const unsig
         add(row, z);
         if constexpr (EPI == EPI_GATED) add(row + 32, z2);
     }
-    const float back = a.xexp ? ldexpf(1.0f, -(int)a.xexp[m]) : a.unit;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-        z[e] *= back;
-        z2[e] *= back;
-    }
     if (a.epi.w_scale[0]) {
-        unscale8(*reinterpret_cast<const u32x2_t*>(a.epi.w_scale[0] + n), z);
-        if constexpr (EPI == EPI_GATED) unscale8(*reinterpret_cast<const u32x2_t*>(a.epi.w_scale[1] + n), z2);
+        const int e = -(int)a.xexp[m];
+        unscale8(*reinterpret_cast<const u32x2_t*>(a.epi.w_scale[0] + n), e, z);
+        if constexpr (EPI == EPI_GATED) unscale8(*reinterpret_cast<const u32x2_t*>(a.epi.w_scale[1] + n), e, z2);
+    } else {
+        const float back = a.xexp ? ldexpf(1.0f, -(int)a.xexp[m]) : a.unit;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            z[e] *= back;
+            z2[e] *= back;
+        }
     }
     if (a.epi.N % 8 == 0) epilogue8<EPI, true>(a.epi, m, n, z, z2);
     else epilogue8<EPI, false>(a.epi, m, n, z, z2);

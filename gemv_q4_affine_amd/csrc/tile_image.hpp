@@ -41,8 +41,8 @@ struct EpilogueArgs {
     const void* residual;
     void* y;
     void* pre[2];
-    // Scale bytes of the weights' rows (padded to whole panels): the image holds a row under 2^13
-    // in the place of 2^(byte - 127).  Null: as they are.
+    // MXFP4: a scale byte for each row of the weights' image (padded to whole panels), which holds
+    // it under 2^13 in the place of 2^(byte - 127).  Null: as they are.
     const uint8_t* w_scale[2];
 };
 constexpr int kRowScale = 127 + 13;
@@ -88,24 +88,30 @@ hipError_t launch_tile_join(int nmat, const TileArgs& a, hipStream_t s);
 enum : int {
     IMG_F16 = 0,       // in binary16
     IMG_REST = 1,      // rows n: after K terms the roundings' remainders; the activations' image then holds its rows twice
-    IMG_ROWS = 2,      // MXFP4, rows n: under the scales of its rows (launch_pack_x's)
+    IMG_ROWS = 2,      // MXFP4: a power of two for each row, from `scales`, into scales.out
     IMG_QUARTER = 3    // MXFP4, rows n: quarters in bfloat16
 };
-hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, int form,
-                               const uint8_t* row_scale, uint8_t* img, hipStream_t s);
-// The largest scale byte of every row of MXFP4 weights: out[mat * panels * 32 + n].
-struct RowScaleArgs {
+// The largest scale bytes of MXFP4 weights, for IMG_ROWS: found beside the packing of the
+// activations or gradients, which comes first.
+struct ScaleArgs {
     const uint8_t* s[2];
     int mats;                  // 0: none
     int64_t N, nb;             // rows, scales of a row
-    uint8_t* out;
+    uint8_t* out;              // rows n: of row n of matrix i at i * panels * 32 + n; rows k: of block k / 32 at k
+    int parts;                 // rows k: parts that the rows are taken in, at most kScaleParts
+    uint8_t* part;             // [parts][nb], largest byte + 1 (0: NaNs only)
 };
+constexpr int kScaleParts = 16;
+int scale_parts(int64_t M, int64_t nb);       // beside a gradient of M rows
+hipError_t launch_pack_weights(int wf, int mats, const QuantW* w, int64_t N, int64_t K, bool transposed, int form,
+                               const ScaleArgs& scales, uint8_t* img, hipStream_t s);
 // dtype DT_BF16 and no xexp: the rows as they are, in bfloat16.
 hipError_t launch_pack_x(const void* x, int dtype, int64_t M, int64_t K, bool twice, uint8_t* img, int8_t* xexp,
-                         const RowScaleArgs& scales, hipStream_t s);
+                         const ScaleArgs& scales, hipStream_t s);
 // dz of every projection: the image, the dz outputs and the column sums.
 int64_t grad_sums_bytes(int nmat, int64_t M, int64_t N);
-hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, hipStream_t s);
+hipError_t launch_pack_dz(const LinearGradArgs& a, uint8_t* img, int8_t* xexp, float* sums, const ScaleArgs& scales,
+                          hipStream_t s);
 // What launch_pack_dz leaves in `sums` to be joined, by launch_join_sums or with a split product's parts.
 SumsArgs sums_args(const LinearGradArgs& a, const float* sums);
 hipError_t launch_join_sums(const SumsArgs& a, hipStream_t s);
@@ -168,10 +174,10 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int left, const u32x4
         if (e < left) q[e] = (uint16_t)(r[e >> 1] >> (16 * (e & 1)));
 }
 
-// Eight sums under the scale bytes of their columns' weights.
-__device__ __forceinline__ void unscale8(const u32x2_t& bytes, float (&v)[8]) {
+// Eight sums times 2^e and their columns' powers of two (in one step: halfway they may leave the range).
+__device__ __forceinline__ void unscale8(const u32x2_t& bytes, int e, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; e++) v[e] = ldexpf(v[e], (int)((bytes[e >> 2] >> (8 * (e & 3))) & 0xFFu) - kRowScale);
+    for (int t = 0; t < 8; t++) v[t] = ldexpf(v[t], (int)((bytes[t >> 2] >> (8 * (t & 3))) & 0xFFu) - kRowScale + e);
 }
 
 // The epilogue of eight consecutive columns n .. n + 7 of row m (`left` of

@@ -77,12 +77,11 @@ int mx_dequantize(int type, const uint8_t* codes, const uint8_t* scales, void* v
  * With MX x the matrix instruction adds the 64 or 128 products of a step at a
  * fixed precision below the largest of them: MXFP8 x loses what lies about 2^-16
  * under it (a sum's error is 5e-6 of it on ordinary data), MXFP4 x nothing.
- * With 16-bit x W may have any scales; only with binary16 x above 64 rows are
- * blocks of W whose scale is less than 2^-36 of their row's largest rounded (to
- * multiples of 2^-37 of that one).
- * In the gradients W must fit binary16 (scales up to 2^13; from 2^-23 on it holds
- * every code exactly, below it rounds them) and dz is scaled per row by a power of
- * two, as in q4_linear.
+ * W may have any scales.  Only with binary16 x above 64 rows are blocks of W whose
+ * scale is less than 2^-36 of their row's largest rounded (to multiples of 2^-37 of
+ * that one), and in the gradients blocks whose scale is less than 2^-36 of the
+ * largest of the same 32 columns; dz is rounded to binary16 after a power of two for
+ * each row, as in q4_linear.
  *
  * (The terms of a sum have to stay in binary32's range, 3.4e38.)
  * A row of x with an infinity or a NaN (a NaN code or scale) spoils no other

@@ -171,3 +171,41 @@ def test_largest_scales_and_infinities(M):
         bad[row, k] = math.nan
         got = Q.mx_linear(w, bad)
         assert torch.isnan(got[row]).all() and torch.equal(got[others], clean[others])
+
+
+# ---- gradients ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,N,blocks", [(1, 33, 255), (5, 64, 255), (70, 2048, 255), (300, 511, 255), (700, 100, 510)])
+def test_gradients_under_every_scale(M, N, blocks):
+    """Columns of W under scales of their own: dx = dz W, dz in binary16 (2^-12 of each term)."""
+    w, W = weights((torch.arange(blocks, device="cuda") % 255)[None].expand(N, blocks).contiguous(), M)
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    seen = torch.zeros(blocks * 32, dtype=torch.bool, device="cuda")
+    for e in (-100, -50, 0, 50, 100):
+        dy = (torch.randn(M, N, generator=gen, device="cuda") * 2.0 ** e).bfloat16()
+        got = Q.mx_linear_backward(w, dy, bias_grad=True)
+        seen |= by_element(got["dx"], dy.double(), W.T, f"{M} 2^{e}", 2.0 ** -12).any(0)
+    assert seen.all()
+
+
+@pytest.mark.parametrize("M,N,blocks", [(1, 33, 5), (9, 100, 16), (70, 2048, 17), (300, 511, 40), (65, 9000, 129), (40, 40000, 15)])
+def test_gradients_of_rows_of_different_scales(M, N, blocks):
+    """Rows of W over 2^36 of scales in every block of columns, all of whose terms count: dy balances them."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    e = torch.tensor([0, 18, -18, 3, -7], device="cuda")[torch.arange(N, device="cuda") % 5]
+    u, U = weights((110 - e // 2)[:, None] + torch.randint(0, 3, (N, blocks), generator=gen, device="cuda"), M + 1)
+    w, W = weights((120 + e)[:, None] - torch.randint(0, 3, (N, blocks), generator=gen, device="cuda"), M)
+    bad = (w[0], w[1].clone())
+    bad[1][N // 2, blocks // 2] = 255
+    dy = (torch.randn(M, N, generator=gen, device="cuda") * torch.exp2(-e.double() / 3)).bfloat16()
+    got = Q.mx_linear_backward(w, dy)["dx"]
+    by_element(got, dy.double(), W.T, f"{M} {N}", 2.0 ** -12)
+    spoilt = Q.mx_linear_backward(bad, dy)["dx"].view(M, blocks, 32)
+    fine = torch.arange(blocks, device="cuda") != blocks // 2
+    assert torch.isnan(spoilt[:, ~fine]).all() and torch.equal(spoilt[:, fine], got.view(M, blocks, 32)[:, fine])
+    # both matrices of a gated product, of which either may have the larger scales
+    gp, up = (torch.randn(M, N, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    for a, A, b, B in ((w, W, u, U), (u, U, w, W)):
+        g = Q.mx_gated_backward(a, b, dy, gp, up, act=Q.Q4_ACT_RELU)
+        dg, du = (dy.double() * up.double() * (gp > 0)), dy.double() * gp.double().clamp(min=0)
+        by_element(g["dx"], torch.cat((dg, du), 1), torch.cat((A, B), 0).T, "gated", 2.0 ** -12)
