@@ -10,8 +10,6 @@ namespace q4 {
 // codes of Q4_MXFP4 and Q4_MXFP8 (include/q4_mx.h), beside DT_BF16 and DT_F16
 enum : int { XT_MXFP4 = 8, XT_MXFP8 = 9 };
 
-inline int64_t mx_code_bytes(int type, int64_t n) { return type == XT_MXFP4 ? n / 2 : n; }
-
 hipError_t launch_mx_quantize(const void* v, int dtype, int type, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K,
                               hipStream_t s);
 hipError_t launch_mx_dequantize(int type, const uint8_t* codes, const uint8_t* scales, void* v, int dtype, int64_t M,

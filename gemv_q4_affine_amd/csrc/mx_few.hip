@@ -400,38 +400,10 @@ __global__ __launch_bounds__(512, 1) void k_mx_few(const MxLinearArgs args, cons
 
 namespace {
 
-// Waves along the sum first, as many as it has groups.  (16 x 12288 x 4096 with 8-bit x: 8.5 us
-// with eight of them, 11.1 with four and two along the rows; up to four rows no difference.)
-// Then one to three row tiles a wave, so that the busiest CU has the fewest of them to do, and
-// of equals the most: a wave then has more loads in flight, and a fragment of x serves more
-// products.  us with one, two and three tiles, 8-bit x but where said:
-//   1 x 4096 x 4096   3.5  4.0  4.3     1 x 12288 x 4096         7.8   7.1   7.3
-//   1 x 8192 x 4096   6.3  5.4  6.4     1 x 12288 x 4096 gated   12.4  12.7  11.5
-//   16 x 12288 x 4096 9.9  9.9  8.6     1 x 12288 x 4096 binary16 17.6 15.6  12.9
-//   16 x 32768 x 4096 19.9 16.4 17.0    4 x 32768 x 4096 bfloat16 25.7 17.6  19.9
-MxFewPlan plan_few(int nmat, int64_t M, int64_t N, int64_t K) {
-    const int P = M <= 4 ? 4 : 1;
-    const int64_t groups = (K / 32 + 16 * P - 1) / (16 * P), tiles = (N + 16 / P - 1) / (16 / P), cus = current_cu_count();
-    MxFewPlan p{};
-    p.kw = (int)(groups < 8 ? groups : 8);
-    p.rw = 8 / p.kw;
-    const int64_t chunks = (M + 63) / 64;
-    int64_t least = 0;
-    for (int r = nmat == 2 && M > 32 ? 1 : 3; r >= 1; r--) { // (the registers hold no more than one there)
-        const int64_t workgroups = (tiles + p.rw * r - 1) / (p.rw * r), of_cu = (workgroups * chunks + cus - 1) / cus * r;
-        if (least == 0 || of_cu < least) {
-            least = of_cu;
-            p.r = r;
-        }
-    }
-    return p;
-}
-
-// (at most 2^25 / 12 workgroups of 512: far below a launch's 2^32 threads)
 template <int XT, int P, int MT, int NM, int R>
 void launch(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
-    const int64_t cols = (int64_t)p.rw * R * (16 / P);
-    hipLaunchKernelGGL((k_mx_few<XT, P, MT, NM, R>), dim3((unsigned)((a.a.N + cols - 1) / cols), (unsigned)((a.a.M + 63) / 64)), dim3(64 * p.kw * p.rw), 0, s, a, p);
+    hipLaunchKernelGGL((k_mx_few<XT, P, MT, NM, R>), dim3((unsigned)few_columns(p, a.a.M, a.a.N), (unsigned)few_chunks(a.a.M)),
+                       dim3(few_threads(p)), 0, s, a, p);
 }
 template <int XT, int P, int MT, int NM>
 void launch_r(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
@@ -456,31 +428,14 @@ void launch_x(const MxLinearArgs& a, const MxFewPlan& p, hipStream_t s) {
 
 }  // namespace
 
-// Up to 64 rows (64 x 12288 x 4096 with 8-bit x: 13.0 us here, 18.9 as tiles; 64 x 4096 x 12288:
-// 18.4 and 18.9).  Gated and above 32 rows a wave has one row tile, and where that makes more
-// than one round of workgroups the tiles are faster (64 x 4096 x 4096: 11.4 here, 17.1 as tiles;
-// 64 x 12288 x 4096: 28.3 and 22.5).
-//
-// Above 64 rows 64 at a time in one launch, by the turns (row tiles and groups) of the busiest CU's waves.
-// bfloat16 x, whose other route makes images: to 128 rows, and where there are four turns at most
-// (128 x 12288 x 4096 30.1 us here, 50.3 there; gated 65.0, 91.2; 256 x 4096 x 4096, four turns, 22.9, 33.4;
-// 256 x 6176 x 1280, four, 23.4, 27.4; 512 x 4096 x 4096, eight, 42.4, 40.9; 512 x 6176 x 1280, eight,
-// 51.6, 28.8).  binary16 x takes twice the products: never (128 x 2048 x 8192 36.8, 31.7).
-// MX x: long sums of at most two turns (128 x 4096 x 4096 9.5, as tiles 15.8; 128 x 2048 x 8192 12.8, 17.0;
-// but 128 x 6176 x 1280 11.8, 7.6, and gated 128 x 4096 x 4096 20.0, 19.4).
 bool mx_few_takes(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {
     const bool mx = x_type == XT_MXFP8 || x_type == XT_MXFP4;
-    if (M <= 64 && (nmat == 1 || M <= 32 || !mx)) return true;
-    if (M > 64 && !(mx ? nmat == 1 && K >= 4096 : x_type == DT_BF16)) return false;
-    const MxFewPlan p = plan_few(nmat, M, N, K);
-    const int64_t cus = current_cu_count(), cols = (int64_t)16 * p.rw * p.r, workgroups = (N + cols - 1) / cols * ((M + 63) / 64);
-    if (M <= 64) return workgroups <= cus;
-    const int64_t groups = (K / 32 + 15) / 16, turns = (workgroups + cus - 1) / cus * p.r * ((groups + p.kw - 1) / p.kw);
-    return mx ? turns <= 2 : M <= 128 || turns <= 4;
+    return few_takes(mx ? FEW_MX : x_type == DT_BF16 ? FEW_BF16 : FEW_F16, nmat, M, N, K, current_cu_count());
 }
 
 hipError_t launch_mx_few(const MxLinearArgs& a, hipStream_t s) {
-    const MxFewPlan p = plan_few(a.a.nmat, a.a.M, a.a.N, a.a.K);
+    const MxFewPlan p = plan_few(a.a.nmat, a.a.M, a.a.N, a.a.K, current_cu_count());
+    if (!launchable(few_columns(p, a.a.M, a.a.N), few_threads(p))) return hipErrorInvalidValue;
     if (a.x_type == XT_MXFP8) launch_x<XT_MXFP8>(a, p, s);
     else if (a.x_type == XT_MXFP4) launch_x<XT_MXFP4>(a, p, s);
     else if (a.x_type == DT_BF16) launch_x<DT_BF16>(a, p, s);

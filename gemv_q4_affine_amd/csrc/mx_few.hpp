@@ -2,6 +2,7 @@
 #pragma once
 
 #include "mx_common.hpp"
+#include "mx_few_plan.hpp"
 
 namespace q4 {
 
@@ -9,10 +10,6 @@ namespace q4 {
 // linear.hip: 16-bit x there must have more than 64 rows).
 bool mx_few_takes(int x_type, int nmat, int64_t M, int64_t N, int64_t K);
 
-// Waves of a workgroup along the sum and along the rows of W, row tiles of a wave.
-struct MxFewPlan {
-    int kw, rw, r;
-};
 hipError_t launch_mx_few(const MxLinearArgs& a, hipStream_t s);
 
 // 16-bit x: W's codes are multiplied in bfloat16, which holds them under every scale up to

@@ -15,6 +15,7 @@
 
 #include "block_common.hpp"
 #include "gemm_common.hpp"
+#include "launch_limits.hpp"
 
 namespace q4 {
 
@@ -22,10 +23,6 @@ constexpr int kUnit = 1024;                 // bytes of a unit
 
 // Slices of a sum over K terms.
 inline int64_t image_slices(int64_t K) { return (K + 31) / 32 * 2; }
-
-// A launch has less than 2^32 threads along a dimension; one with more runs,
-// without an error, on what is left of them modulo 2^32.
-inline bool launchable(int64_t blocks, int threads) { return blocks * threads < int64_t(1) << 32; }
 
 // Epilogue of the product (one of them is chosen at compile time).
 enum : int {
