@@ -167,21 +167,6 @@ static hipError_t launch_few(const LinearArgs& a, const FewPlan& p, int64_t m0, 
                                 : launch_few_affine8(t, p, split, s);
 }
 
-static EpilogueArgs epilogue_args(const LinearArgs& a) {
-    EpilogueArgs e{};
-    e.act = a.act;
-    e.dtype = a.dtype;
-    e.M = a.M;
-    e.N = a.N;
-    for (int i = 0; i < 2; i++) {
-        e.bias[i] = a.bias[i];
-        e.pre[i] = a.pre[i];
-    }
-    e.residual = a.residual;
-    e.y = a.y;
-    return e;
-}
-
 hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
     if (a.M <= kFewCallMaxM) {
         if (a.wf == WF_MXFP4) return hipErrorInvalidValue;   // those rows are launch_mx_few's

@@ -8,21 +8,6 @@ namespace {
 
 bool is_mx(int x_type) { return x_type == XT_MXFP4 || x_type == XT_MXFP8; }
 
-EpilogueArgs epilogue_args(const LinearArgs& a) {
-    EpilogueArgs e{};
-    e.act = a.act;
-    e.dtype = a.dtype;
-    e.M = a.M;
-    e.N = a.N;
-    for (int i = 0; i < 2; i++) {
-        e.bias[i] = a.bias[i];
-        e.pre[i] = a.pre[i];
-    }
-    e.residual = a.residual;
-    e.y = a.y;
-    return e;
-}
-
 }  // namespace
 
 int64_t mx_linear_workspace_bytes(int x_type, int nmat, int64_t M, int64_t N, int64_t K) {

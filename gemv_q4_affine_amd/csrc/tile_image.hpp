@@ -43,6 +43,20 @@ struct EpilogueArgs {
     const uint8_t* w_scale[2];
 };
 constexpr int kRowScale = 127 + 13;
+inline EpilogueArgs epilogue_args(const LinearArgs& a) {
+    EpilogueArgs e{};
+    e.act = a.act;
+    e.dtype = a.dtype;
+    e.M = a.M;
+    e.N = a.N;
+    for (int i = 0; i < 2; i++) {
+        e.bias[i] = a.bias[i];
+        e.pre[i] = a.pre[i];
+    }
+    e.residual = a.residual;
+    e.y = a.y;
+    return e;
+}
 
 // The bias gradients: sums over groups of rows, [groups][nmat][N], joined in order
 // into the columns of out (null: none).
