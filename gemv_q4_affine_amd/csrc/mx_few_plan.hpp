@@ -53,22 +53,32 @@ inline MxFewPlan plan_few(int nmat, int64_t M, int64_t N, int64_t K, int64_t cus
 // than one round of workgroups the tiles are faster (64 x 4096 x 4096: 11.4 here, 17.1 as tiles;
 // 64 x 12288 x 4096: 28.3 and 22.5).
 //
-// Above 64 rows 64 at a time in one launch, by the turns (row tiles and groups) of the busiest CU's waves.
-// bfloat16 x, whose other route makes images: to 128 rows, and where there are four turns at most
-// (128 x 12288 x 4096 30.1 us here, 50.3 there; gated 65.0, 91.2; 256 x 4096 x 4096, four turns, 22.9, 33.4;
-// 256 x 6176 x 1280, four, 23.4, 27.4; 512 x 4096 x 4096, eight, 42.4, 40.9; 512 x 6176 x 1280, eight,
-// 51.6, 28.8).  binary16 x takes twice the products: never (128 x 2048 x 8192 36.8, 31.7).
-// MX x: long sums of at most two turns (128 x 4096 x 4096 9.5, as tiles 15.8; 128 x 2048 x 8192 12.8, 17.0;
-// but 128 x 6176 x 1280 11.8, 7.6, and gated 128 x 4096 x 4096 20.0, 19.4).
+// Above 64 rows 64 at a time in one launch, by the turns (row tiles and groups) of the busiest CU's
+// waves and its rounds of workgroups; us here and by the other route.
+// bfloat16 x, whose other route makes images: to 128 rows (128 x 12288 x 4096 26.7 and 48.9, x 32768 x
+// 1280 41.9, 44.0, x 512 x 512 9.4, 13.1, x 300 x 16384 28.3, 31.5; gated x 12288 x 1280 31.7, 36.2), and
+// above where there are at most four turns, gated three (256 x 4096 x 4096, four turns, 22.1, 33.2; 512 x
+// 4096 x 4096, eight, 43.8, 40.2; gated 256 x 4096 x 2048, two, 21.9, 33.0; 256 x 8192 x 2048, four, 42.0,
+// 38.6), but short sums only in two rounds (256 x 16384 x 544, two, 21.5, 23.4; 384 x 8192 x 544, three,
+// 24.2, 17.8).
+// binary16 x takes twice the products: not (128 x 1024 x 1024 19.9 and 16.4, x 2048 x 8192 36.1, 33.2, x
+// 300 x 16384 68, 35; but x 4096 x 4096 22.6, 31.2).
+// MX x, whose other route reads the planes too: linear, at most two turns of long sums (128 x 4096 x 4096 9.1
+// and 14.5, x 2048 x 2304 9.1, 10.1, x 4096 x 2048, 7.3, 9.8, x 2048 x 1536 5.9, 8.3, x 1024 x 1024 7.0, 7.1,
+// 256 x 4096 x 2560, four turns, 12.3, 11.1); where a row's last group is not whole only of longer ones (128 x
+// 4096 x 4128 13.8, 17.6, x 2048 x 1792 9.6, 8.9).  Gated 128 x 4096 x 4096 20.0 here, 19.4 as tiles.
 inline bool few_takes(int x, int nmat, int64_t M, int64_t N, int64_t K, int64_t cus) {
     const bool mx = x == FEW_MX;
     if (M <= 64 && (nmat == 1 || M <= 32 || !mx)) return true;
-    if (M > 64 && !(mx ? nmat == 1 && K >= 4096 : x == FEW_BF16)) return false;
+    if (M > 64 && !(mx ? nmat == 1 && K >= (K % 512 == 0 ? 1536 : 4096) : x == FEW_BF16)) return false;
     const MxFewPlan p = plan_few(nmat, M, N, K, cus);
     const int64_t workgroups = few_columns(p, M, N) * few_chunks(M);
     if (M <= 64) return workgroups <= cus;
-    const int64_t groups = (K / 32 + 15) / 16, turns = (workgroups + cus - 1) / cus * p.r * ((groups + p.kw - 1) / p.kw);
-    return mx ? turns <= 2 : M <= 128 || turns <= 4;
+    const int64_t groups = (K / 32 + 15) / 16, rounds = (workgroups + cus - 1) / cus;
+    const int64_t turns = rounds * p.r * ((groups + p.kw - 1) / p.kw);
+    if (mx) return turns <= 2;
+    if (M <= 128) return true;
+    return nmat == 2 ? turns <= 3 : turns <= 4 && (K >= 1024 || rounds <= 2);
 }
 
 }  // namespace q4
