@@ -197,8 +197,11 @@ hipError_t launch_linear(const LinearArgs& a, void* workspace, hipStream_t s) {
         t.xexp = nullptr;
         t.unit = 4.0f;
     }
-    hipError_t e = launch_pack_x(a.x, a.dtype, a.M, a.K, form == IMG_REST, ws + l.x_at, const_cast<int8_t*>(t.xexp), scales, s);
-    if (e == hipSuccess) e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, form, scales, ws, s);
+    auto weights = [&] { return launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, false, form, scales, ws, s); };
+    hipError_t e = form != IMG_ROWS ? weights() : hipSuccess;
+    if (e == hipSuccess)
+        e = launch_pack_x(a.x, a.dtype, a.M, a.K, form == IMG_REST, ws + l.x_at, const_cast<int8_t*>(t.xexp), scales, s);
+    if (e == hipSuccess && form == IMG_ROWS) e = weights();  // behind their rows' scales
     if (e != hipSuccess) return e;
     return launch_tile_gemm(l.plan, a.nmat, t, s);
 }
@@ -213,9 +216,11 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStrea
     const bool mx = a.wf == WF_MXFP4;
     ScaleArgs scales = mx ? scale_args(a, l, ws) : ScaleArgs{};
     scales.parts = scale_parts(a.M, a.K / 32);
-    hipError_t e = launch_pack_dz(a, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at),
-                                  reinterpret_cast<float*>(ws + l.sums_at), scales, s);
-    if (e == hipSuccess) e = launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, mx ? IMG_ROWS : IMG_F16, scales, ws, s);
+    auto weights = [&] { return launch_pack_weights(a.wf, a.nmat, a.w, a.N, a.K, true, mx ? IMG_ROWS : IMG_F16, scales, ws, s); };
+    hipError_t e = mx ? hipSuccess : weights();
+    if (e == hipSuccess)
+        e = launch_pack_dz(a, ws + l.x_at, reinterpret_cast<int8_t*>(ws + l.exp_at),
+                           reinterpret_cast<float*>(ws + l.sums_at), scales, s);
     if (e != hipSuccess) return e;
     // the bias gradients' join goes with the parts' where the product is split
     // (MXFP4, 1001 x 8192 x 2048: 71.0 us against 73.4 with a launch of its own, 200 x 1024 x 1024 23.0 and 25.9)
@@ -223,6 +228,7 @@ hipError_t launch_linear_grad(const LinearGradArgs& a, void* workspace, hipStrea
     TileArgs t = tile_args(l, ws);
     if (l.plan.parts > 1) t.sums = sums;
     else if ((e = launch_join_sums(sums, s)) != hipSuccess) return e;
+    if (mx && (e = weights()) != hipSuccess) return e;       // behind their columns' scales
     t.epi.w_scale[0] = scales.out;
     t.epi.act = ACT_NONE;
     t.epi.dtype = DT_BF16;

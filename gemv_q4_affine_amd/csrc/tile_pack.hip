@@ -176,31 +176,42 @@ __global__ __launch_bounds__(256) void k_pack_weights_t(QuantW w0, QuantW w1, in
     const bool in_k = blk < nb;
     uint32_t raw[8];
     RowScale<WF> sc[8];
-    int most = 0;
+    // MXFP4: the tile's eight columns of scales and their parts' largest, a byte a thread
+    __shared__ __attribute__((aligned(16))) uint8_t parts[8][kScaleParts];
+    if (WF == WF_MXFP4 && tid < 8 * kScaleParts) {
+        const int64_t b = kt * 8 + tid / kScaleParts, part = tid % kScaleParts;
+        parts[0][tid] = scales.part[(part < scales.parts ? part : scales.parts - 1) * nb + (b < nb ? b : nb - 1)];
+    }
+    int byte[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int64_t n = n0 + i < N ? n0 + i : N - 1, b = in_k ? blk : nb - 1;
+        raw[i] = *reinterpret_cast<const uint32_t*>(w.q + (n * nb + b) * (128 / kPer) + wb * 4);
+        if constexpr (WF == WF_MXFP4) byte[i] = reinterpret_cast<const uint8_t*>(w.s)[n * nb + b];
+        else sc[i] = row_scale<WF>(w, n, b, K);
+    }
     if constexpr (WF == WF_MXFP4) {
+        __syncthreads();
+        const u32x4_t all = *reinterpret_cast<const u32x4_t*>(parts[p]);
+        int most = 0;
 #pragma unroll
         for (int i = 0; i < kScaleParts; i++) {
-            const int p = i < scales.parts ? i : scales.parts - 1;       // (loads without a branch go together)
-            const int m = scales.part[p * nb + (in_k ? blk : nb - 1)];
+            const int m = (int)(all[i >> 2] >> (8 * (i & 3)) & 0xFFu);
             most = m > most ? m : most;
         }
         most = most > 0 ? most - 1 : 0;
         if (nt == 0 && mat == 0 && o == 0 && in_k)
             *reinterpret_cast<u32x2_t*>(scales.out + k0) = u32x2_t{most * 0x01010101u, most * 0x01010101u};
+#pragma unroll
+        for (int i = 0; i < 8; i++) sc[i] = {scale_below(byte[i], most), 0.0f};
     }
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const bool ok = in_k && n0 + i < N;
-        const int64_t n = n0 + i < N ? n0 + i : N - 1, b = in_k ? blk : nb - 1;
-        raw[i] = *reinterpret_cast<const uint32_t*>(w.q + (n * nb + b) * (128 / kPer) + wb * 4);
-        if constexpr (WF == WF_MXFP4) sc[i] = {scale_below(reinterpret_cast<const uint8_t*>(w.s)[n * nb + b], most), 0.0f};
-        else sc[i] = row_scale<WF>(w, n, b, K);
-        if (!ok) {
+    for (int i = 0; i < 8; i++)
+        if (!in_k || n0 + i >= N) {
             sc[i].s = 0.0f;
             sc[i].b = 0.0f;
             raw[i] = 0u;
         }
-    }
     uint8_t* base = lds + p * kPanelB + (o >> 1) * kUnit + (o & 1) * 512;
     auto put = [&](int j, auto code) __attribute__((always_inline)) {
         float f[8];
