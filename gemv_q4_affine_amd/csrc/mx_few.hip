@@ -5,8 +5,8 @@
 // Mathematics.  With MX x a 16x16x128 scaled MFMA takes the codes and scales as
 // they are.  With 16-bit x the codes are converted with their scale to bfloat16,
 // which holds them exactly (2 bits and any scale up to 2^125; see bf16_scale), and
-// multiplied by bfloat16 x in four 16x16x32 MFMAs; binary16 x is split into two bfloat16 parts, x = hi + lo
-// exactly, and takes eight.  Products are exact, sums binary32.
+// multiplied by bfloat16 x in four 16x16x32 MFMAs; binary16 x is split into two
+// bfloat16 parts, x = hi + lo exactly, and takes eight.  Products are exact, sums binary32.
 //
 // Layout.  Lane l of the MFMA holds one block of 32 of A's row j = l & 15, block
 // slot g = l >> 4.  Taken as 16 rows of W, neighbouring lanes lie on different rows.
@@ -22,10 +22,12 @@
 // direct copies to LDS, a wave's own part of it.
 //
 // Bounds.  One row: memory, and the round trip of a short launch: a pair of 12288 x 4096
-// in 11.5 us (57 MB, 4.9 TB/s; a large copy reaches 5.2), one in 7.3, one 32768 x 4096 in
+// in 11.5 us (53.5 MB, 4.65 TB/s; a large copy reaches 5.2), one in 7.3, one 32768 x 4096 in
 // 13.6 (5.2 TB/s), one 2048 x 8192 with bfloat16 x in 4.9.  5 to 64 rows: every workgroup
-// reads all of x through LDS (12288 x 4096 with 8-bit x: 16 rows 8.5, 32 9.6, 64 13.0 us);
-// 16-bit x also the conversions beside the products (12.2 us at 32 rows; binary16 twice the products).
+// reads all of x through LDS (12288 x 4096 with 8-bit x: 16 rows 8.5, 32 9.6, 64 13.0 us), and a
+// wave waits for each stage of x with nothing else in flight, as it does for the weights of its
+// next group; 16-bit x also the conversions beside the products (10.8 us at 32 rows with bfloat16,
+// 16.2 with binary16, whose products are twice as many).
 #include "gemm_common.hpp"
 #include "mx_few.hpp"
 #include "tile_image.hpp"

@@ -18,7 +18,8 @@
 // and their joins across the waves lie between a row's loads and its stores
 // (two barriers a row; two workgroups of 512 threads are resident on a CU, and each
 // has its next row's loads in flight meanwhile).
-// Two passes in binary32 would be nearer to memory but flip codes.  One row: 3.9 us.
+// Binary32 throughout would be nearer to memory but flips codes; binary32 with binary64 only for
+// values near a border is not tried.  One row: 3.9 us.
 #include "mx_common.hpp"
 #include "tile_image.hpp"
 #include "wave_exchange.hpp"

@@ -26,10 +26,12 @@
 // Shorter sums pay the start and the end of a tile, 9000 to 22000 cycles: 2048 x 4096 x
 // 12288 88 us, the gated pair of 2048 x 12288 x 4096 186 with both projections stored, 160 without.
 // 4-bit x: 2048 x 12288 x 4096 in 79 us; a step of 4 x 4 panels takes 1880 cycles for 1024 of
-// MFMAs.  LDS meets no bank conflict, and memory is not what it waits for: 4096 x 4096 x 16384
-// takes 151 us, 147 with every copy from the same lines, 124 without copies.  Eight waves a workgroup instead of
-// four (half the tile each, two waves a SIMD to hide each other's waits) were no
-// faster: 81 us, and 98.5 against 97 at 2048 x 12288 x 4096 with 8-bit x.
+// MFMAs.  Neither memory nor LDS is what it lacks: 4096 x 4096 x 16384 takes 151 us, 147 with every copy
+// from the same lines, 124 without copies, and LDS is busy for 0.17 of its cycles, without a bank conflict.
+// Its waves wait at the counters and barriers for 0.19 of their time, as many cycles as with 8-bit x, whose
+// MFMAs take twice as long (matrix pipe 0.52 busy; 8 bits 0.79, 0.15): the schedule, in MFMAs, is that of
+// 8-bit x.  Eight waves a workgroup instead of four (half the tile each, two waves a SIMD to hide each other's
+// waits) were no faster: 81 us, and 98.5 against 97 at 2048 x 12288 x 4096 with 8-bit x.
 #include "mx_tile.hpp"
 #include "tile_epilogue.hpp"
 
