@@ -377,7 +377,8 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Cost of a plan in cycles: rounds of workgroups over the CUs, each a start and an
 // end and its steps, as measured (8-bit x: 4 x 4 panels 2450 a step, of which 2048 its
-// MFMAs; 4-bit x: 1880 of which 1024, bound by the instructions beside them).
+// MFMAs; 4-bit x: 1880 of which 1024).  Rounds are counted by one workgroup a CU, also of 2 x 2
+// panels, two of which share one: what sharing gains them is not measured.
 double plan_cost(int nt, int mt, int parts, bool k8, int64_t w_panels, int64_t x_panels, int64_t steps, int cus) {
     const int64_t tiles = ((w_panels + 2 * nt - 1) / (2 * nt)) * ((x_panels + 2 * mt - 1) / (2 * mt));
     const int64_t rounds = (tiles * parts + cus - 1) / cus;
